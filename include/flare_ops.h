@@ -1,0 +1,95 @@
+/*
+ * flare_ops.h - C ABI of the operators around the FLARE / FLARE++ mixer on
+ * B200 (sm_100a): the preparation of queries and keys (per-head RMS norm and
+ * position rotation), forward and backward.
+ *
+ * Conventions (status codes, flare_bf16, streams and workspaces as in
+ * flare.h):
+ *   - Tensors of rows are [B][H][N][D] bf16 in DEVICE memory with D dense
+ *     elements per row and free strides over batch, head and row, given in
+ *     elements: a head-major tensor has strides (H N D, N D, D), a slice of a
+ *     token-major projection [B][N][Ht D] has (N Ht D, D, Ht D).  Every row
+ *     starts on a 16-byte boundary (pointers aligned, strides multiples of 8
+ *     elements).  The stride of a size-one dimension is not read.  Outputs
+ *     must not overlap each other or the inputs.
+ *   - D in {16, 32, 64, 128}.
+ *   - Arguments come in one struct whose members are all 8 bytes wide.
+ *     Pointers marked optional may be NULL.
+ *   - Every call only enqueues work on the stream (which must belong to the
+ *     calling thread's current device) and may be captured into a graph;
+ *     nothing is allocated and no state is kept between calls.  Two calls
+ *     that may run at the same time need two workspaces.
+ *   - Results are deterministic: no floating-point atomics.
+ */
+#ifndef FLARE_OPS_H_
+#define FLARE_OPS_H_
+
+#include "flare.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * Preparation of queries and keys.  Per row x (one token n, one head h) of
+ * Q and of K:
+ *   y_d = x_d * rsqrt(mean_d(x^2) + eps) * gain_d
+ *   then every pair (a, b) of y, p = 0 .. rot/2 - 1, is rotated:
+ *   (a cos t - b sin t, a sin t + b cos t),  t = sum_i pos[n][i] * freqs[i][p]
+ * The pairs are elements (p, p + rot/2), or (2p, 2p + 1) when interleaved;
+ * elements rot .. D-1 are not rotated.  Angles are formed in 64 bits.
+ *
+ * Q or K may be absent (NULL with its outputs and gain NULL and its head
+ * count 0).  rot = 0 (freqs NULL): norm only.  rot is even, at most D; a
+ * multiple of 16 unless interleaved.
+ *   pos_kind 0: pos[n] = n                          (axes 1, positions NULL)
+ *   pos_kind 1: positions int32 [B][N]              (axes 1)
+ *   pos_kind 2: positions float [B][N][axes]        (axes 1 .. 4)
+ * gain: float [D], or [H][D] when gain_per_head; NULL: no gain.
+ * lengths: optional int32 [B], clamped to [0, N]; rows n >= lengths[b] are
+ * not read and are written as zeros.
+ */
+typedef struct {
+  int64_t B, N, D, Hq, Hk;
+  int64_t rot, axes, interleaved, pos_kind;
+  double eps;
+  const float* freqs;      /* [axes][rot / 2] */
+  const void* positions;
+  const int32_t* lengths;
+  const flare_bf16* Q;
+  int64_t q_stride[3];     /* batch, head, row */
+  const flare_bf16* K;
+  int64_t k_stride[3];
+  const float* q_gain;
+  const float* k_gain;
+  int64_t q_gain_per_head, k_gain_per_head;
+  /* forward: Qr, Kr written; backward: their gradients, read */
+  flare_bf16* Qr;
+  int64_t qr_stride[3];
+  flare_bf16* Kr;
+  int64_t kr_stride[3];
+  /* backward only: gradients, written; dq_gain, dk_gain are float tensors of the gains' shapes (NULL: not wanted) */
+  flare_bf16* dQ;
+  int64_t dq_stride[3];
+  flare_bf16* dK;
+  int64_t dk_stride[3];
+  float* dq_gain;
+  float* dk_gain;
+} flare_qk_norm_rope_args;
+
+/* Workspace of flare_qk_norm_rope_bwd (partial sums of the gains' gradients); 0 for unsupported sizes. */
+FLARE_API size_t flare_qk_norm_rope_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t Hk, int64_t D);
+FLARE_API flare_status flare_qk_norm_rope_fwd(const flare_qk_norm_rope_args* args, void* stream);
+/*
+ * Gradients: with g the gradient of a rotated row, u = g rotated back, r =
+ * rsqrt(mean(x^2) + eps), w = u * gain:
+ *   dx = r * (w - x r mean(w x r)),   dgain = sum over rows of u * x r
+ * The workspace may be NULL when neither dq_gain nor dk_gain is wanted.
+ */
+FLARE_API flare_status flare_qk_norm_rope_bwd(const flare_qk_norm_rope_args* args, void* workspace,
+                                              size_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* FLARE_OPS_H_ */

@@ -35,3 +35,9 @@ from ._binding import (  # noqa: F401
 )
 from . import cp  # noqa: F401,E402  (context-parallel forward and backward over torch.distributed)
 from .autograd import flare_mixer, flarepp_mixer  # noqa: F401,E402  (torch.autograd wrappers)
+from .qk_norm_rope import (  # noqa: F401,E402  (queries and keys: per-head norm and position rotation)
+    flare_qk_norm_rope,
+    flare_qk_norm_rope_bwd,
+    flare_qk_norm_rope_fwd,
+    flare_qk_norm_rope_workspace_bytes,
+)

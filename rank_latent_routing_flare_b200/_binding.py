@@ -115,6 +115,14 @@ def load_library(build_if_missing: bool = True):
         lib.flarepp_mixer_fwd_profiled.restype = i
         lib.flare_mixer_fwd_static.argtypes = [vp, vp, vp, vp, i, i, i, i, i, vp, f, vp, vp]
         lib.flare_mixer_fwd_static.restype = i
+        # operators of include/flare_ops.h: argument structs are passed as packed bytes
+        i64, pk = ctypes.c_int64, ctypes.c_char_p
+        lib.flare_qk_norm_rope_workspace_bytes.restype = sz
+        lib.flare_qk_norm_rope_workspace_bytes.argtypes = [i64] * 5
+        lib.flare_qk_norm_rope_fwd.restype = i
+        lib.flare_qk_norm_rope_fwd.argtypes = [pk, vp]
+        lib.flare_qk_norm_rope_bwd.restype = i
+        lib.flare_qk_norm_rope_bwd.argtypes = [pk, vp, sz, vp]
         lib.flare_last_device_status.argtypes = [vp, vp]
         lib.flare_last_device_status.restype = i
         lib.flare_status_string.argtypes = [i]
