@@ -1,7 +1,7 @@
 /*
  * flare_ops.h - C ABI of the operators around the FLARE / FLARE++ mixer on
  * B200 (sm_100a): the preparation of queries and keys (per-head RMS norm and
- * position rotation), forward and backward.
+ * position rotation) and exact softmax attention, forward and backward.
  *
  * Conventions (status codes, flare_bf16, streams and workspaces as in
  * flare.h):
@@ -88,6 +88,62 @@ FLARE_API flare_status flare_qk_norm_rope_fwd(const flare_qk_norm_rope_args* arg
  */
 FLARE_API flare_status flare_qk_norm_rope_bwd(const flare_qk_norm_rope_args* args, void* workspace,
                                               size_t workspace_bytes, void* stream);
+
+/*
+ * Exact softmax attention.  Query head h reads key head h / (Hq / Hk).  Row
+ * i of Q stands at position p_i = q_offset + i.  Score of row i and key j:
+ *   s = scale * <q_i, k_j>;  with cap > 0: s = cap * tanh(s / cap)
+ *   with slopes: s -= slopes[h] * |p_i - j|
+ * Row i sees key j when all of these hold:
+ *   j < lengths[b], i < q_lengths[b]             (where given; clamped to [0, Nk] and [0, Nq])
+ *   not causal, or j <= p_i, or j < prefix[b]
+ *   no documents, or j and p_i lie in the same document: a document is a run
+ *     of equal ids in documents[b][0 .. Nk); ids below zero belong to none
+ * Y_i = softmax_j(s) V, L_i = log sum_j exp(s).  A row that sees no key has
+ * Y_i = 0, L_i = -inf and zero gradients, and contributes none.
+ *
+ * Keys that no row may see (j >= lengths[b], ids below zero) and rows i >=
+ * q_lengths[b] may hold anything, infinities and NaN included.
+ */
+typedef struct {
+  int64_t B, Hq, Hk, Nq, Nk, D;
+  int64_t causal;
+  double scale;                /* <= 0: 1 / sqrt(D) */
+  double cap;                  /* <= 0: not capped */
+  const flare_bf16* Q;
+  int64_t q_stride[3];
+  const flare_bf16* K;
+  int64_t k_stride[3];
+  const flare_bf16* V;
+  int64_t v_stride[3];
+  const int32_t* lengths;      /* optional [B] */
+  const int32_t* q_lengths;    /* optional [B] */
+  const int32_t* q_offsets;    /* optional [B]; NULL: Nk - Nq */
+  const int32_t* documents;    /* optional [B][Nk] */
+  const int32_t* prefix;       /* optional [B]; read when causal */
+  const float* slopes;         /* optional [Hq] */
+  /* forward: written (L optional); backward: read */
+  flare_bf16* Y;
+  int64_t y_stride[3];
+  float* L;                    /* [B][Hq][Nq] */
+  /* backward only */
+  const flare_bf16* dY;
+  int64_t dy_stride[3];
+  flare_bf16* dQ;
+  int64_t dq_stride[3];
+  flare_bf16* dK;
+  int64_t dk_stride[3];
+  flare_bf16* dV;
+  int64_t dv_stride[3];
+} flare_attention_args;
+
+/* Workspace of flare_attention_fwd (backward = 0) or flare_attention_bwd (1); 0 for unsupported sizes. */
+FLARE_API size_t flare_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hk, int64_t Nq, int64_t Nk, int64_t D,
+                                                 int backward);
+FLARE_API flare_status flare_attention_fwd(const flare_attention_args* args, void* workspace, size_t workspace_bytes,
+                                           void* stream);
+FLARE_API flare_status flare_attention_bwd(const flare_attention_args* args, void* workspace, size_t workspace_bytes,
+                                           void* stream);
 
 #ifdef __cplusplus
 }

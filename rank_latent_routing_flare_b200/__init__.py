@@ -41,3 +41,10 @@ from .qk_norm_rope import (  # noqa: F401,E402  (queries and keys: per-head norm
     flare_qk_norm_rope_fwd,
     flare_qk_norm_rope_workspace_bytes,
 )
+from .attention import (  # noqa: F401,E402  (exact softmax attention with caps, biases and interval masks)
+    flare_attention,
+    flare_attention_bwd,
+    flare_attention_fwd,
+    flare_attention_fwd_train,
+    flare_attention_workspace_bytes,
+)

@@ -123,6 +123,11 @@ def load_library(build_if_missing: bool = True):
         lib.flare_qk_norm_rope_fwd.argtypes = [pk, vp]
         lib.flare_qk_norm_rope_bwd.restype = i
         lib.flare_qk_norm_rope_bwd.argtypes = [pk, vp, sz, vp]
+        lib.flare_attention_workspace_bytes.restype = sz
+        lib.flare_attention_workspace_bytes.argtypes = [i64] * 6 + [i]
+        for fn in (lib.flare_attention_fwd, lib.flare_attention_bwd):
+            fn.restype = i
+            fn.argtypes = [pk, vp, sz, vp]
         lib.flare_last_device_status.argtypes = [vp, vp]
         lib.flare_last_device_status.restype = i
         lib.flare_status_string.argtypes = [i]

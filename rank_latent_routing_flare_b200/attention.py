@@ -1,0 +1,173 @@
+"""Exact softmax attention: capped scores, a distance bias, and causal, prefix,
+packed-document and padding masks; forward, backward, and single new tokens
+over a cache.
+
+The N x N attention that the mixer approximates through its latents, on the
+same [B, H, N, D] tensors (any strides with dense rows).  Argument checks and
+marshalling only: the kernels are behind include/flare_ops.h.
+"""
+from __future__ import annotations
+
+import struct
+
+import torch
+
+from . import _binding as b
+from ._rows import ROW_WIDTHS, call, check_rows, check_small, ptr, rows, same_device, workspace as _ws
+
+# flare_attention_args
+_ARGS = struct.Struct("=7q2d12q6q4qq4q12q")
+_NONE4 = (0, 0, 0, 0)
+
+
+def flare_attention_workspace_bytes(B: int, Hq: int, Hk: int, Nq: int, Nk: int, D: int, backward: bool = False) -> int:
+    return int(b.load_library().flare_attention_workspace_bytes(B, Hq, Hk, Nq, Nk, D, int(backward)))
+
+
+def _check(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal):
+    if any(t.dim() != 4 for t in (Q, K, V)):
+        raise ValueError("Q, K and V are [B, H, N, D]")
+    B, Hq, Nq, D = Q.shape
+    Hk, Nk = K.shape[1:3]
+    if D not in ROW_WIDTHS:
+        raise ValueError(f"D is {D}, expected one of {ROW_WIDTHS}")
+    if Hk == 0 or Hq % Hk:
+        raise ValueError(f"{Hq} query heads are not a multiple of {Hk} key heads")
+    check_rows("Q", Q, (B, Hq, Nq, D))
+    check_rows("K", K, (B, Hk, Nk, D))
+    check_rows("V", V, (B, Hk, Nk, D))
+    dev = Q.device
+    same_device(dev, K=K, V=V)
+    for name, t in (("lengths", lengths), ("q_lengths", q_lengths), ("q_offsets", q_offsets), ("prefix", prefix)):
+        if t is not None:
+            check_small(name, t, torch.int32, (B,), dev)
+    if documents is not None:
+        check_small("documents", documents, torch.int32, (B, Nk), dev)
+    if slopes is not None:
+        check_small("slopes", slopes, torch.float32, (Hq,), dev)
+    if prefix is not None and not causal:
+        raise ValueError("prefix goes with causal=True")
+
+
+def _pack(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap, Y, L, back=None):
+    B, Hq, Nq, D = Q.shape
+    Hk, Nk = K.shape[1:3]
+    dY, dQ, dK, dV = (_NONE4,) * 4 if back is None else map(rows, back)
+    return _ARGS.pack(B, Hq, Hk, Nq, Nk, D, bool(causal), scale, cap, *rows(Q), *rows(K), *rows(V), ptr(lengths),
+                      ptr(q_lengths), ptr(q_offsets), ptr(documents), ptr(prefix), ptr(slopes), *rows(Y), ptr(L), *dY,
+                      *dQ, *dK, *dV)
+
+
+def _device_check(device_check, ws, stream, where):
+    if device_check:
+        st = b.flare_last_device_status(ws, stream)
+        if st != 0:
+            raise b.FlareError(st, where + " (device status)")
+
+
+def _forward(where, Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap, Y, L,
+             workspace, stream, check, device_check):
+    if check:
+        _check(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal)
+        if Y is not None:
+            check_rows("Y", Y, tuple(Q.shape), output=True)
+        check_small("L", L, torch.float32, tuple(Q.shape[:3]), Q.device)
+    dev = Q.device
+    if Y is None:
+        Y = torch.empty(Q.shape, dtype=torch.bfloat16, device=dev)
+    B, Hq, Nq, D = Q.shape
+    ws = _ws(workspace, flare_attention_workspace_bytes(B, Hq, K.shape[1], Nq, K.shape[2], D), dev)
+    args = _pack(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap, Y, L)
+    call(b.load_library().flare_attention_fwd, where, dev, stream, args, ws.data_ptr(), ws.numel())
+    _device_check(device_check, ws, stream, where)
+    return Y
+
+
+def flare_attention_fwd(Q, K, V, lengths=None, q_lengths=None, q_offsets=None, documents=None, prefix=None,
+                        slopes=None, causal: bool = False, scale: float = 0.0, cap: float = 0.0, Y=None, L_out=None,
+                        workspace=None, stream=None, check: bool = True, device_check: bool = False):
+    """Y = softmax(scores) V for Q [B,Hq,Nq,D], K, V [B,Hk,Nk,D] (bf16 views with
+    dense rows; query head h reads key head h // (Hq // Hk)) -> Y [B,Hq,Nq,D] bf16.
+
+    Row i stands at position p = q_offsets[b] + i (default Nk - Nq + i).  Scores:
+    scale <q, k> (scale <= 0: 1/sqrt(D)), then cap * tanh(. / cap) if cap > 0,
+    then minus slopes[h] * |p - j| (float32 [Hq]).  A row sees key j if j <
+    lengths[b], i < q_lengths[b] (int32 [B]), with ``causal`` j <= p or j <
+    prefix[b] (int32 [B]), and with ``documents`` (int32 [B,Nk]) j and p lie in
+    the same run of equal ids >= 0.  A row that sees nothing comes out as zeros;
+    keys that no row may see and rows behind q_lengths may hold anything.
+
+    One new token over a cache: Nq = 1, lengths = tokens in the cache, q_offsets
+    = lengths - 1.  ``L_out`` (float32 [B,Hq,Nq]) receives the rows'
+    log-sum-exps.  With ``device_check`` the device status is read after the
+    call (synchronises); its only error is an expired bounded wait."""
+    return _forward("flare_attention_fwd", Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal,
+                    scale, cap, Y, L_out, workspace, stream, check, device_check)
+
+
+def flare_attention_fwd_train(Q, K, V, lengths=None, q_lengths=None, q_offsets=None, documents=None, prefix=None,
+                              slopes=None, causal: bool = False, scale: float = 0.0, cap: float = 0.0, Y=None,
+                              L_out=None, workspace=None, stream=None, check: bool = True, device_check: bool = False):
+    """flare_attention_fwd that returns (Y, L), what flare_attention_bwd takes."""
+    L = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device) if L_out is None else L_out
+    Y = _forward("flare_attention_fwd_train", Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes,
+                 causal, scale, cap, Y, L, workspace, stream, check, device_check)
+    return Y, L
+
+
+def flare_attention_bwd(Q, K, V, Y, L, dY, lengths=None, q_lengths=None, q_offsets=None, documents=None, prefix=None,
+                        slopes=None, causal: bool = False, scale: float = 0.0, cap: float = 0.0, dQ=None, dK=None,
+                        dV=None, workspace=None, stream=None, check: bool = True, device_check: bool = False):
+    """Gradients (dQ, dK, dV), bf16, given dY and the forward's Y and L (same
+    inputs, masks, scale and cap).  dK and dV are summed over the query heads of
+    a key head.  dQ, dK and dV may be preallocated strided views."""
+    if check:
+        _check(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal)
+        for name, t in (("Y", Y), ("dY", dY)):
+            check_rows(name, t, tuple(Q.shape))
+            same_device(Q.device, **{name: t})
+        if L is None:
+            raise ValueError("L is the forward's log-sum-exps")
+        check_small("L", L, torch.float32, tuple(Q.shape[:3]), Q.device)
+        for name, t, x in (("dQ", dQ, Q), ("dK", dK, K), ("dV", dV, K)):
+            if t is not None:
+                check_rows(name, t, tuple(x.shape), output=True)
+                same_device(Q.device, **{name: t})
+    dev = Q.device
+    dQ = torch.empty(Q.shape, dtype=torch.bfloat16, device=dev) if dQ is None else dQ
+    dK = torch.empty(K.shape, dtype=torch.bfloat16, device=dev) if dK is None else dK
+    dV = torch.empty(K.shape, dtype=torch.bfloat16, device=dev) if dV is None else dV
+    B, Hq, Nq, D = Q.shape
+    ws = _ws(workspace, flare_attention_workspace_bytes(B, Hq, K.shape[1], Nq, K.shape[2], D, backward=True), dev)
+    args = _pack(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap, Y, L,
+                 (dY, dQ, dK, dV))
+    call(b.load_library().flare_attention_bwd, "flare_attention_bwd", dev, stream, args, ws.data_ptr(), ws.numel())
+    _device_check(device_check, ws, stream, "flare_attention_bwd")
+    return dQ, dK, dV
+
+
+class Attention(torch.autograd.Function):
+    """Y of Q, K and V, differentiable in all three."""
+
+    @staticmethod
+    def forward(ctx, Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap):
+        if slopes is not None and slopes.requires_grad:
+            raise ValueError("slopes: gradients with respect to the distance bias are not computed")
+        Y, L = flare_attention_fwd_train(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal,
+                                         scale, cap)
+        ctx.save_for_backward(Q, K, V, Y, L, lengths, q_lengths, q_offsets, documents, prefix, slopes)
+        ctx.causal, ctx.scale, ctx.cap = causal, scale, cap
+        return Y
+
+    @staticmethod
+    def backward(ctx, dY):
+        Q, K, V, Y, L, *masks = ctx.saved_tensors
+        dY = dY.to(torch.bfloat16).contiguous()
+        dQ, dK, dV = flare_attention_bwd(Q, K, V, Y, L, dY, *masks, ctx.causal, ctx.scale, ctx.cap)
+        return (dQ, dK, dV) + (None,) * 9
+
+
+def flare_attention(Q, K, V, lengths=None, q_lengths=None, q_offsets=None, documents=None, prefix=None, slopes=None,
+                    causal: bool = False, scale: float = 0.0, cap: float = 0.0):
+    """Differentiable flare_attention_fwd (see Attention)."""
+    return Attention.apply(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap)

@@ -1,0 +1,82 @@
+// Parameters of the exact softmax attention kernels (attn_fwd.cu,
+// attn_step.cu, attn_bwd.cu, attn_rows.cu).
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace flare {
+
+// Masks.  Every mask leaves row i of a batch entry one interval [lo, hi) of
+// keys, and lo and hi do not decrease with i: the rows that see a key tile
+// and the keys that a row tile sees are ranges too.
+struct AttnMask {
+  int Nq, Nk, causal;
+  const int32_t *lengths, *q_lengths, *q_offsets, *prefix;
+  const int2* doc;   // [B][Nk] first and one-past-last position of the document a position lies in
+                     // (equal: in none), or nullptr
+};
+
+struct AttnSide {    // rows [B][H][N][D] with strides in elements
+  const uint16_t* p;
+  long sb, sh, sn;
+};
+
+struct AttnParams {
+  int B, Hq, Hk, G, D;           // G = Hq / Hk
+  AttnMask mask;
+  float scale;                   // applied to <q, k>
+  float cap;                     // <= 0: none
+  const float* slopes;           // [Hq] or nullptr
+  uint16_t* y;
+  long ys[3];
+  float* L;                      // [B][Hq][Nq] or nullptr
+  // work split along the keys: partial results of every split, joined by attn_join
+  int splits;
+  float* part_o;                 // [splits][B][Hq][Nq][D], each split's normalised output
+  float* part_l;                 // [splits][B][Hq][Nq], its log2 sum of weights
+  uint32_t* err;
+  unsigned long long timeout_ns;
+};
+
+// One row's statistics for the backward, [B][Hq][Nq padded to kAttnRowPad]:
+// P = 2^(x - l2) (l2 = +inf: the row sees nothing), delta = <dY, Y>, the
+// interval of keys it sees.
+struct __align__(16) AttnRow {
+  float l2, delta;
+  int lo, hi;
+};
+constexpr int kAttnRowPad = 128;
+
+struct AttnBwdParams {
+  AttnParams a;
+  AttnSide dy, yin;
+  uint16_t *dq, *dk, *dv;
+  long dqs[3], dks[3], dvs[3];
+  AttnRow* rows;
+  int rows_pad;                  // rows per head: Nq rounded up to kAttnRowPad
+};
+
+struct AttnMaps {                // tensor maps of the kernels' operands
+  CUtensorMap q, k, v, dy;
+};
+
+// Runs of equal ids -> the document table of AttnMask.
+cudaError_t launch_attn_documents(const int32_t* ids, int2* doc, int B, int N, cudaStream_t s);
+
+int attn_fwd_key_tile(int D);    // keys per tile; the query tile is kAttnQTile rows
+constexpr int kAttnQTile = 128;
+cudaError_t launch_attn_fwd(const AttnMaps& m, const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t s);
+
+constexpr int kAttnStepRows = 16;   // query rows per key head of the kernel for few rows
+cudaError_t launch_attn_step(const AttnParams& p, const AttnSide& q, const AttnSide& k, const AttnSide& v,
+                             cudaStream_t s);
+
+int attn_bwd_stream_tile(int D);
+cudaError_t launch_attn_rows(const AttnBwdParams& p, cudaStream_t s);
+cudaError_t launch_attn_bwd_dq(const AttnMaps& m, const AttnBwdParams& p, cudaStream_t s);
+cudaError_t launch_attn_bwd_dkv(const AttnMaps& m, const AttnBwdParams& p, cudaStream_t s);
+
+}  // namespace flare

@@ -1,0 +1,71 @@
+// The dQ pass of the attention's backward, and the row statistics both passes
+// read.
+#include "attn_bwd_kernel.cuh"
+
+namespace flare {
+namespace {
+
+// One row's statistics: l2 = L log2(e), moved by the distance that the bias
+// positions leave out (+inf: the row sees nothing), delta = <dY, Y> in fp32,
+// and its interval of keys.  D / 8 lanes a row, 16-byte loads.
+template <int D>
+__global__ void __launch_bounds__(256) attn_rows_kernel(const AttnBwdParams bp) {
+  constexpr int L = D / 8, ROWS = 256 / L;
+  const AttnParams& p = bp.a;
+  const long blocks = (bp.rows_pad + ROWS - 1) / ROWS;
+  const long bh = blockIdx.x / blocks;
+  const int i = static_cast<int>(blockIdx.x % blocks) * ROWS + threadIdx.x / L, l = threadIdx.x % L;
+  const int b = static_cast<int>(bh / p.Hq), h = static_cast<int>(bh % p.Hq);
+  if (bh == 0 && blockIdx.x == 0 && threadIdx.x < 4) p.err[threadIdx.x] = 0u;
+  const BatchMask m = batch_mask(p.mask, b);
+  const int2 iv = row_interval(m, i);
+  const bool sees = i < p.mask.Nq && iv.x < iv.y;
+  float delta = 0.f;
+  if (sees) {
+    const uint4 a = *reinterpret_cast<const uint4*>(bp.dy.p + b * bp.dy.sb + h * bp.dy.sh + i * bp.dy.sn + 8 * l);
+    const uint4 y = *reinterpret_cast<const uint4*>(bp.yin.p + b * bp.yin.sb + h * bp.yin.sh + i * bp.yin.sn + 8 * l);
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) delta = fmaf(bf16_lo(u[k]), bf16_lo(v[k]), fmaf(bf16_hi(u[k]), bf16_hi(v[k]), delta));
+  }
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) delta += __shfl_xor_sync(~0u, delta, o);
+  if (l == 0 && i < bp.rows_pad) {
+    AttnRow r{INFINITY, 0.f, iv.x, iv.y};
+    if (sees) {
+      float L2 = p.L[bh * p.mask.Nq + i];
+      if (p.slopes) L2 += p.slopes[h] * bias_shift(m, i, iv);
+      if (L2 != -INFINITY) {
+        r.l2 = L2 * kLog2e;
+        r.delta = delta;
+      }
+    }
+    bp.rows[bh * bp.rows_pad + i] = r;
+  }
+}
+
+}  // namespace
+
+int attn_bwd_stream_tile(int D) { return D >= 64 ? BwdCfg<64>::T : BwdCfg<32>::T; }
+
+cudaError_t launch_attn_rows(const AttnBwdParams& p, cudaStream_t s) {
+  auto go = [&](auto d) {
+    constexpr int D = decltype(d)::value, ROWS = 256 / (D / 8);
+    const long blocks = (p.rows_pad + ROWS - 1) / ROWS;
+    attn_rows_kernel<D><<<static_cast<unsigned>(blocks * p.a.B * p.a.Hq), 256, 0, s>>>(p);
+    return cudaGetLastError();
+  };
+  switch (p.a.D) {
+    case 16: return go(std::integral_constant<int, 16>{});
+    case 32: return go(std::integral_constant<int, 32>{});
+    case 64: return go(std::integral_constant<int, 64>{});
+    case 128: return go(std::integral_constant<int, 128>{});
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_attn_bwd_dq(const AttnMaps& m, const AttnBwdParams& p, cudaStream_t s) {
+  return launch_attn_bwd_pass<false>(m.q, m.dy, m.k, m.v, p, s);
+}
+
+}  // namespace flare

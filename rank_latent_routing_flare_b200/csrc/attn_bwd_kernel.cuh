@@ -1,0 +1,392 @@
+// Exact softmax attention, backward, on tcgen05.  With P = 2^(x - l2) from the
+// forward's row sums, g = <dY_i, v_j>, delta_i = <dY_i, Y_i> and x' the
+// derivative of the capped score (1 without a cap):
+//
+//   dV_j = sum_i P_ij dY_i      dS_ij = P_ij (g_ij - delta_i) x'_ij
+//   dQ_i = scale sum_j dS_ij k_j     dK_j = scale sum_i dS_ij q_i
+//
+// One kernel, two passes, so that every output is summed in one accumulator
+// in a fixed order (no atomics).  A CTA keeps a tile of 128 rows and streams
+// tiles of T rows of the other side:
+//
+//   dQ pass  rows: queries (Q, dY), stream: keys (K, V)
+//     S = Q K^T, G = dY V^T, out1 += dS K
+//   dK/dV pass  rows: keys (K, V), stream: the rows (Q, dY) of every query
+//     head of the key head, S = K Q^T, G = V dY^T, out1 += dS Q, out2 += P dY
+//
+// The rows are TMEM lanes (UMMA M = 128).  The two warpgroups take stream
+// tiles in turn: each has its own S and G columns and both add to the same
+// accumulators.  Weights and dS are written over S and G as bf16 and read from
+// there as the products' A operands; the MMA thread issues tile n's products
+// and right behind them the scores of tile n + 2 into the same columns (the
+// tensor pipe runs in order), while the other warpgroup works on tile n + 1.
+// Row statistics (l2, delta, interval) are held in registers in the dQ pass
+// and come with the stream in the dK/dV pass.
+//
+// Streamed rows that take no part (padding) are zeroed in shared memory
+// before the products read them: a weight of 0 does not erase a NaN.
+//
+// D >= 64: T = 64, up to 512 TMEM columns, one CTA per SM.  D <= 32: T = 48,
+// 256 columns, two CTAs per SM; the exponentials bound those.
+#pragma once
+
+#include "attn_common.cuh"
+
+namespace flare {
+
+template <int D_>
+struct BwdCfg {
+  static constexpr int D = D_;
+  using Tile = RowTile<D>;
+  static constexpr int T = D >= 64 ? 64 : 48;
+  static constexpr int CH = D >= 64 ? 32 : 16;           // columns of a tile computed at once
+  static constexpr int CTAS = D >= 64 ? 1 : 2;
+  static constexpr int NST = D == 128 ? 4 : 6;
+  static constexpr int X_B = Tile::bytes(128), Y_B = Tile::bytes(T), R_B = 1024;
+  static constexpr int OFF_X = 0;                         // X1 | X2
+  static constexpr int OFF_Y = OFF_X + 2 * X_B;           // NST x (Y1 | Y2)
+  static constexpr int OFF_R = OFF_Y + 2 * NST * Y_B;     // NST x row statistics (dK/dV pass)
+  static constexpr int OFF_BAR = OFF_R + NST * R_B;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * (1 + 2 * NST + 2 + 2 + 1);
+  static constexpr int BYTES = OFF_MISC + 32 + 4 * NST;
+  static constexpr uint32_t COL_S = 0, COL_OUT1 = 4 * T, COL_OUT2 = 4 * T + D;   // buffer g: S at 2 T g, G at 2 T g + T
+  static constexpr uint32_t TMEM_COLS = COL_OUT2 + D <= 256 ? 256 : 512;
+  static constexpr int THREADS = 320;                     // warps 0-3, 4-7: softmax; 8: loads; 9: MMAs
+  static_assert(COL_OUT2 + D <= TMEM_COLS && TMEM_COLS * CTAS <= 512, "TMEM columns");
+  static_assert(Y_B % (8 * Tile::ROWB) == 0 && X_B % 1024 == 0 && T * 16 <= R_B, "tiles hold whole swizzle atoms");
+};
+
+template <int D, bool KV, bool MOD>
+__global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
+    attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_x2,
+                    const __grid_constant__ CUtensorMap tm_y1, const __grid_constant__ CUtensorMap tm_y2,
+                    const AttnBwdParams bp) {
+  using Cfg = BwdCfg<D>;
+  using Tile = RowTile<D>;
+  constexpr int T = Cfg::T, NST = Cfg::NST, CH = Cfg::CH;
+  const AttnParams& p = bp.a;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sx = sm + Cfg::OFF_X;
+  uint8_t* sy = sm + Cfg::OFF_Y;
+  uint8_t* sr = sm + Cfg::OFF_R;
+  uint64_t* x_full = reinterpret_cast<uint64_t*>(sm + Cfg::OFF_BAR);
+  uint64_t* y_full = x_full + 1;          // [NST]
+  uint64_t* y_empty = y_full + NST;       // [NST] products of the tile done
+  uint64_t* s_full = y_empty + NST;       // [2] scores and G of the warpgroup's next tile ready
+  uint64_t* p_full = s_full + 2;          // [2] weights and dS stored (one arrive per warp)
+  uint64_t* all_done = p_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Cfg::OFF_MISC);
+  int* abort_flag = reinterpret_cast<int*>(sm + Cfg::OFF_MISC + 4);
+  volatile int* range = reinterpret_cast<volatile int*>(sm + Cfg::OFF_MISC + 8);       // [2]
+  volatile int* last_load = reinterpret_cast<volatile int*>(sm + Cfg::OFF_MISC + 32);  // [NST]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the dQ pass owns query heads and begins with the last rows, the dK/dV
+  // pass owns key heads and begins with the first keys: under a causal mask
+  // those have the most to do
+  const int heads = KV ? p.Hk : p.Hq, n_tiles = gridDim.x / (p.B * heads);
+  const int ti = static_cast<int>(blockIdx.x) / (p.B * heads), bh = static_cast<int>(blockIdx.x) % (p.B * heads);
+  const int x0 = (KV ? ti : n_tiles - 1 - ti) * 128;
+  const int b = bh / heads, hx = bh % heads;
+  const BatchMask mask = batch_mask(p.mask, b);
+
+  if (threadIdx.x < 2) {
+    int v = 0;
+    if (KV) {   // rows that see keys [x0, x0 + 128): hi > x0 from the first on, lo < x0 + 128 up to the last
+      int lo = 0, hi = mask.qlen;
+      while (lo < hi) {
+        const int mid = lo + (hi - lo) / 2;
+        const int2 iv = row_interval(mask, mid);
+        if (threadIdx.x == 0 ? iv.y > x0 : iv.x >= x0 + 128) hi = mid; else lo = mid + 1;
+      }
+      v = threadIdx.x == 0 ? lo / T : (lo + T - 1) / T;
+    } else {
+      const int r1 = min(x0 + 128, mask.qlen);
+      if (x0 < r1) {
+        const int lo = row_interval(mask, x0).x, hi = row_interval(mask, r1 - 1).y;
+        if (lo < hi) v = threadIdx.x == 0 ? lo / T : (hi + T - 1) / T;
+      }
+    }
+    range[threadIdx.x] = v;
+  }
+  if (threadIdx.x == 64) {
+    mbar_init(x_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 4);
+    }
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(y_full + i, 1);
+      mbar_init(y_empty + i, 1);
+      last_load[i] = -1;
+    }
+    mbar_init(all_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx wc{p.err, abort_flag, p.timeout_ns};
+  const int t_lo = range[0], per_head = max(0, range[1] - range[0]);
+  const int N = KV ? per_head * p.G : per_head;   // stream tiles
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0 && N > 0) {
+      tma_prefetch_desc(&tm_x1);
+      tma_prefetch_desc(&tm_x2);
+      tma_prefetch_desc(&tm_y1);
+      tma_prefetch_desc(&tm_y2);
+      mbar_arrive_expect_tx(x_full, 2 * Cfg::X_B);
+      Tile::load(sx, &tm_x1, x_full, x0, hx, b, 128);
+      Tile::load(sx + Cfg::X_B, &tm_x2, x_full, x0, hx, b, 128);
+      for (int n = 0; n < N; ++n) {
+        const int st = n % NST;
+        if (n >= NST && !mbar_wait(y_empty + st, (n / NST - 1) & 1, wc)) break;
+        const int g = KV ? n / per_head : 0, row = (t_lo + n - g * per_head) * T;
+        const int hy = KV ? hx * p.G + g : hx / p.G;
+        mbar_arrive_expect_tx(y_full + st, 2 * Cfg::Y_B + (KV ? T * 16 : 0));
+        Tile::load(sy + 2 * st * Cfg::Y_B, &tm_y1, y_full + st, row, hy, b, T);
+        Tile::load(sy + (2 * st + 1) * Cfg::Y_B, &tm_y2, y_full + st, row, hy, b, T);
+        if (KV)
+          bulk_load(sr + st * Cfg::R_B, bp.rows + (static_cast<long>(b) * p.Hq + hy) * bp.rows_pad + row, T * 16,
+                    y_full + st);
+        last_load[st] = n;
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMAs
+    if (lane == 0 && N > 0) {
+      const uint32_t idesc_s = idesc_bf16_f32(128, T, false, false);
+      const uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
+      const uint64_t x1 = Tile::desc_k(sx), x2 = Tile::desc_k(sx + Cfg::X_B);
+      const uint64_t y_k = Tile::desc_k(sy), y_mn = Tile::desc_mn(sy, T);
+      constexpr uint64_t TILE = Cfg::Y_B >> 4;
+      auto issue_scores = [&](int n) -> bool {
+        const int st = n % NST;
+        if (!mbar_wait_mma(y_full + st, (n / NST) & 1, wc)) return false;
+        tc_fence_after();
+        const uint32_t col = tmem + Cfg::COL_S + (n & 1) * 2 * T;
+        const uint64_t y1 = y_k + 2 * st * TILE, y2 = y1 + TILE;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss(col, x1 + Tile::kstep_k(kk, 128), y1 + Tile::kstep_k(kk, T), idesc_s, kk > 0 ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss(col + T, x2 + Tile::kstep_k(kk, 128), y2 + Tile::kstep_k(kk, T), idesc_s, kk > 0 ? 1u : 0u);
+        umma_commit(s_full + (n & 1));
+        return true;
+      };
+      bool ok = mbar_wait_mma(x_full, 0, wc) && issue_scores(0);
+      if (ok && N > 1) ok = issue_scores(1);
+      for (int n = 0; ok && n < N; ++n) {
+        const int st = n % NST;
+        if (!mbar_wait_mma(p_full + (n & 1), (n >> 1) & 1, wc)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t col = tmem + Cfg::COL_S + (n & 1) * 2 * T;
+        const uint64_t y1 = y_mn + 2 * st * TILE, y2 = y1 + TILE;
+#pragma unroll
+        for (int ks = 0; ks < T / 16; ++ks)
+          umma_ts(tmem + Cfg::COL_OUT1, col + T + ks * 8, y1 + ks * Tile::KSTEP_MN, idesc_o, (n > 0 || ks > 0) ? 1u : 0u);
+        if (KV) {
+#pragma unroll
+          for (int ks = 0; ks < T / 16; ++ks)
+            umma_ts(tmem + Cfg::COL_OUT2, col + ks * 8, y2 + ks * Tile::KSTEP_MN, idesc_o, (n > 0 || ks > 0) ? 1u : 0u);
+        }
+        umma_commit(y_empty + st);
+        if (n + 2 < N) ok = issue_scores(n + 2);
+      }
+      umma_commit(all_done);
+      mbar_wait_drain(all_done, 0, p.timeout_ns);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int w = warp >> 2, wq = warp & 3;
+    const int tid = threadIdx.x & 127;
+    const int row = x0 + tid;                       // query (dQ pass) or key of this lane
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+    const uint32_t col_s = lane_base + Cfg::COL_S + w * 2 * T, col_g = col_s + T;
+    const float c2 = p.scale * kLog2e;
+    const float tanh_in = MOD && p.cap > 0.f ? 2.f * c2 / p.cap : 0.f, tanh_out = p.cap * kLog2e;
+    // dQ pass: this row's statistics
+    AttnRow mine{INFINITY, 0.f, 0, 0};
+    float slope2 = 0.f;
+    int pos = 0;
+    if (!KV) {
+      if (row < p.mask.Nq) mine = bp.rows[(static_cast<long>(b) * p.Hq + hx) * bp.rows_pad + row];
+      pos = bias_position(mask, row, make_int2(mine.lo, mine.hi));
+      if (MOD && p.slopes) slope2 = p.slopes[hx] * kLog2e;
+    }
+    bool ok = true;
+    for (int n = w; n < N; n += 2) {
+      const int st = n % NST;
+      const int g = KV ? n / per_head : 0, y0 = (t_lo + n - g * per_head) * T;
+      if (KV && MOD && p.slopes) slope2 = p.slopes[hx * p.G + g] * kLog2e;
+      bool dead = false;                            // the streamed row this thread answers for takes no part
+      if (!KV && tid < T && y0 + tid < mask.nk) {
+        dead = y0 + tid >= mask.len;
+        if (mask.doc) {
+          const int2 d = mask.doc[y0 + tid];
+          dead |= d.x == d.y;
+        }
+      }
+      if (!mbar_wait_warp(s_full + w, (n >> 1) & 1, wc)) { ok = false; break; }
+      tc_fence_after();
+      const AttnRow* rs = reinterpret_cast<const AttnRow*>(sr + st * Cfg::R_B);
+      bool full;
+      if (KV) {
+        // the statistics came with the tile; waiting here makes them visible to this thread
+        if (!mbar_wait_warp(y_full + st, (n / NST) & 1, wc)) { ok = false; break; }
+        full = y0 + T <= mask.qlen && rs[0].hi >= x0 + 128 && rs[T - 1].lo <= x0;
+        dead = tid < T && rs[tid].l2 == INFINITY;
+      } else {
+        full = __all_sync(~0u, mine.lo <= y0 && mine.hi >= y0 + T);
+      }
+#pragma unroll
+      for (int c = 0; c < T; c += CH) {
+        uint32_t s[CH], gg[CH], pk[CH / 2], dk[CH / 2];
+        tmem_ld_cols<CH>(col_s + c, s);
+        tmem_ld_cols<CH>(col_g + c, gg);
+        tmem_wait_ld();
+        regs_loaded(s);
+        regs_loaded(gg);
+#pragma unroll
+        for (int k = 0; k < CH; k += 2) {
+          float pv[2], dv[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int y = c + k + u;
+            float l2 = mine.l2, delta = mine.delta;
+            if (KV) {
+              l2 = rs[y].l2;
+              delta = rs[y].delta;
+            }
+            float x = __uint_as_float(s[k + u]) * c2, dx = 1.f;
+            if (MOD && p.cap > 0.f) {
+              const float t = tanh_exp(__uint_as_float(s[k + u]) * tanh_in);
+              x = t * tanh_out;
+              dx = fmaf(-t, t, 1.f);
+            }
+            if (MOD && p.slopes) {
+              int d;
+              if (KV) {
+                const int2 iv = make_int2(rs[y].lo, rs[y].hi);
+                d = bias_position(mask, y0 + y, iv) - row;
+              } else {
+                d = pos - (y0 + y);
+              }
+              x = fmaf(-slope2, fabsf(static_cast<float>(d)), x);
+            }
+            float pr = ex2_mufu(x - l2);
+            float ds = pr * (__uint_as_float(gg[k + u]) - delta);
+            if (MOD) ds *= dx;
+            if (!full) {
+              const int lo = KV ? rs[y].lo : mine.lo, hi = KV ? rs[y].hi : mine.hi, key = KV ? row : y0 + y;
+              if (key < lo || key >= hi) pr = ds = 0.f;
+            }
+            pv[u] = pr;
+            dv[u] = ds;
+          }
+          pk[k / 2] = pack_bf16x2(pv[0], pv[1]);
+          dk[k / 2] = pack_bf16x2(dv[0], dv[1]);
+        }
+        if (KV) tmem_st_cols<CH / 2>(col_s + c / 2, pk);
+        tmem_st_cols<CH / 2>(col_g + c / 2, dk);
+      }
+      if (dead) {
+        if (!mbar_wait(y_full + st, (n / NST) & 1, wc)) ok = false;   // landed before the scores were computed
+        Tile::zero_row(sy + 2 * st * Cfg::Y_B, tid, T);
+        if (KV) Tile::zero_row(sy + (2 * st + 1) * Cfg::Y_B, tid, T);
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive_warp(p_full + w);
+    }
+    if (ok && N > 0) ok = mbar_wait_warp(all_done, 0, wc);
+    ok = __all_sync(~0u, ok);
+    if (ok) {
+      tc_fence_after();
+      // dK/dV pass: warpgroup 0 writes dK, 1 writes dV.  dQ pass: half the columns each (D = 16: all by 0).
+      const bool second = KV && w == 1;
+      const int d_beg = KV || D == 16 ? 0 : w * (D / 2), d_end = KV ? D : D == 16 ? (w == 0 ? D : 0) : d_beg + D / 2;
+      const uint32_t col = lane_base + (second ? Cfg::COL_OUT2 : Cfg::COL_OUT1);
+      uint16_t* out = second ? bp.dv + b * bp.dvs[0] + hx * bp.dvs[1] + static_cast<long>(row) * bp.dvs[2]
+                      : KV   ? bp.dk + b * bp.dks[0] + hx * bp.dks[1] + static_cast<long>(row) * bp.dks[2]
+                             : bp.dq + b * bp.dqs[0] + hx * bp.dqs[1] + static_cast<long>(row) * bp.dqs[2];
+      const float f = second ? 1.f : p.scale;
+      const bool have = row < (KV ? p.mask.Nk : p.mask.Nq);
+      // a row that takes no part gets zeros, whatever its lane holds
+      const bool zero = N == 0 || (KV ? row >= mask.len || (mask.doc && have && mask.doc[row].x == mask.doc[row].y)
+                                      : mine.l2 == INFINITY);
+      for (int d = d_beg; d < d_end; d += 16) {
+        uint32_t o[16];
+        if (N > 0) {
+          tmem_ld16(col + d, o);
+          tmem_wait_ld();
+          regs_loaded(o);
+        }
+        uint32_t pk[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          pk[i] = zero ? 0u : pack_bf16x2(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f);
+        if (have) {
+          uint4* dst = reinterpret_cast<uint4*>(out + d);
+          dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8 && lane == 0 && N > 0) {   // copies still in flight (only after an abort) must land before exit
+    for (int st = 0; st < NST; ++st)
+      if (last_load[st] >= 0) mbar_wait_drain(y_full + st, (last_load[st] / NST) & 1, p.timeout_ns);
+    mbar_wait_drain(x_full, 0, p.timeout_ns);
+  }
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::TMEM_COLS);
+  }
+}
+
+template <bool KV>
+cudaError_t launch_attn_bwd_pass(const CUtensorMap& x1, const CUtensorMap& x2, const CUtensorMap& y1,
+                                 const CUtensorMap& y2, const AttnBwdParams& p, cudaStream_t s) {
+  const long tiles = ((KV ? p.a.mask.Nk : p.a.mask.Nq) + 127) / 128;
+  const unsigned grid = static_cast<unsigned>(tiles * p.a.B * (KV ? p.a.Hk : p.a.Hq));
+  auto go = [&](auto kern, int bytes, int threads, int ctas) {
+    // at most `ctas` CTAs share an SM, so that each finds its TMEM columns free
+    const int floor = 228 * 1024 / (ctas + 1) + 1024;
+    const int smem = bytes + 1024 > floor ? bytes + 1024 : floor;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, threads, smem, s>>>(x1, x2, y1, y2, p);
+    return cudaGetLastError();
+  };
+  const bool mod = p.a.cap > 0.f || p.a.slopes;
+  auto by_mod = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    using C = BwdCfg<D>;
+    return mod ? go(attn_bwd_kernel<D, KV, true>, C::BYTES, C::THREADS, C::CTAS)
+               : go(attn_bwd_kernel<D, KV, false>, C::BYTES, C::THREADS, C::CTAS);
+  };
+  switch (p.a.D) {
+    case 16: return by_mod(std::integral_constant<int, 16>{});
+    case 32: return by_mod(std::integral_constant<int, 32>{});
+    case 64: return by_mod(std::integral_constant<int, 64>{});
+    case 128: return by_mod(std::integral_constant<int, 128>{});
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace flare

@@ -1,0 +1,113 @@
+// Device code shared by the attention kernels: masks, score modifiers and the
+// layout of row tiles in shared memory.
+#pragma once
+
+#include "attention.h"
+#include "ptx.cuh"
+
+namespace flare {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Masks of one batch entry.
+struct BatchMask {
+  int len, qlen, pre, causal, nk;
+  long off;
+  const int2* doc;
+};
+__device__ __forceinline__ BatchMask batch_mask(const AttnMask& m, int b) {
+  BatchMask r;
+  r.nk = m.Nk;
+  r.len = m.lengths ? max(0, min(m.Nk, m.lengths[b])) : m.Nk;
+  r.qlen = m.q_lengths ? max(0, min(m.Nq, m.q_lengths[b])) : m.Nq;
+  r.off = m.q_offsets ? static_cast<long>(m.q_offsets[b]) : static_cast<long>(m.Nk) - m.Nq;
+  r.pre = m.prefix ? m.prefix[b] : 0;
+  r.causal = m.causal;
+  r.doc = m.doc ? m.doc + static_cast<long>(b) * m.Nk : nullptr;
+  return r;
+}
+// Keys [x, y) that row i sees (x = y: none).
+__device__ __forceinline__ int2 row_interval(const BatchMask& m, int i) {
+  const long p = m.off + i;
+  long lo = 0, hi = m.len;
+  if (m.causal) hi = min(hi, max(max(p + 1, static_cast<long>(m.pre)), 0L));
+  if (m.doc) {
+    if (p < 0) {
+      hi = 0;
+    } else if (p >= m.nk) {
+      lo = hi = m.nk;
+    } else {
+      const int2 d = m.doc[p];
+      lo = d.x;
+      hi = min(hi, static_cast<long>(d.y));
+    }
+  }
+  if (hi < lo || i >= m.qlen) hi = lo;
+  return make_int2(static_cast<int>(lo), static_cast<int>(hi));
+}
+// Position of row i for the distance bias, moved to the nearest key it sees:
+// |p - j| = |p - p'| + |p' - j| for every such key j, and the softmax does
+// not see the first term.  Distances stay exact in fp32 that way, however
+// far the row stands from its keys.
+__device__ __forceinline__ int bias_position(const BatchMask& m, int i, int2 iv) {
+  const long p = m.off + i;
+  return static_cast<int>(max(static_cast<long>(iv.x), min(p, static_cast<long>(iv.y) - 1)));
+}
+__device__ __forceinline__ float bias_shift(const BatchMask& m, int i, int2 iv) {   // |p - p'|
+  const long d = m.off + i - bias_position(m, i, iv);
+  return static_cast<float>(d < 0 ? -d : d);
+}
+
+// tanh from 2^x and a reciprocal: 1 - 2 / (1 + e^(2u)); its error against
+// tanh is about 1e-7 absolute, of a result that the cap multiplies.
+__device__ __forceinline__ float tanh_exp(float u2log2e) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_mufu(u2log2e)));
+  return fmaf(-2.f, r, 1.f);
+}
+
+// After tcgen05.wait::ld: the registers a TMEM load wrote are defined here,
+// so that no use of them is scheduled before the wait.
+template <int N>
+__device__ __forceinline__ void regs_loaded(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Row tiles in shared memory: panels of up to 64 elements (128 bytes, the
+// widest swizzle), each `rows` x PANEL elements as TMA writes them.
+template <int D>
+struct RowTile {
+  static constexpr int PANEL = D < 64 ? D : 64;
+  static constexpr int NP = D / PANEL;
+  static constexpr int ROWB = PANEL * 2;
+  static constexpr uint32_t LAYOUT = ROWB == 32 ? LAYOUT_SW32 : ROWB == 64 ? LAYOUT_SW64 : LAYOUT_SW128;
+  static constexpr int bytes(int rows) { return rows * D * 2; }
+  // descriptor of the tile as an operand whose k runs along D
+  __device__ static uint64_t desc_k(const void* base) { return umma_desc(smem_u32(base), 16, 8 * ROWB, LAYOUT); }
+  // k-step kk (16 elements of D) of that operand, in a tile of `rows` rows
+  __device__ static constexpr uint64_t kstep_k(int kk, int rows) {
+    return static_cast<uint64_t>(((kk * 16 / PANEL) * rows * ROWB + (kk * 16 % PANEL) * 2) >> 4);
+  }
+  // descriptor of the tile as the B operand [D] x [rows] of a product over rows
+  __device__ static uint64_t desc_mn(const void* base, int rows) {
+    return umma_desc(smem_u32(base), rows * ROWB, 8 * ROWB, LAYOUT);
+  }
+  // k-step of 16 rows of that operand
+  static constexpr uint64_t KSTEP_MN = (16 * ROWB) >> 4;
+  // rows [row, row + rows) of (b, h) by TMA into `dst`
+  __device__ static void load(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row, int h, int b, int rows) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) tma_load_4d(dst + p * rows * ROWB, map, bar, p * PANEL, row, h, b);
+  }
+  // zero row r (swizzling permutes 16-byte pieces within a row of a panel only)
+  __device__ static void zero_row(uint8_t* tile, int r, int rows) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int i = 0; i < ROWB / 16; ++i)
+        *reinterpret_cast<uint4*>(tile + p * rows * ROWB + r * ROWB + 16 * i) = make_uint4(0, 0, 0, 0);
+  }
+};
+
+}  // namespace flare
