@@ -87,7 +87,7 @@ extern "C" {
 
 size_t flare_qk_norm_rope_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t Hk, int64_t D) {
   if (check_sizes(B, N, Hq, Hk, D) != FLARE_OK) return 0;
-  return align256(static_cast<size_t>(norm_rope_bwd_ctas(B, N)) * (Hq + Hk) * D * sizeof(float));
+  return align256(norm_rope_part_floats(B, N, Hq, Hk, D) * sizeof(float));
 }
 
 flare_status flare_qk_norm_rope_fwd(const flare_qk_norm_rope_args* args, void* stream) {

@@ -27,16 +27,21 @@ struct NormRopeParams {
   const void* pos;
   const int32_t* lengths;
   float eps;
+  // work split (norm_rope_plan)
+  int groups;           // groups of heads a warp takes at once, queries' first
+  int ctas_y;           // CTAs over the groups
+  int cta_groups;       // groups per CTA
+  int parts;            // shares of a tile's tokens per group: warps per CTA = cta_groups * parts
   int tile;             // tokens per tile
   int tiles_per_b;
   long n_tiles;         // B * tiles_per_b
-  int ctas;             // backward: CTAs launched
-  float* part;          // backward: [ctas][(Hq + Hk) D] partial sums of the gains' gradients
+  int ranges;           // backward: CTAs over the tiles, each taking every ranges-th
+  float* part;          // backward: [ranges][ctas_y][gain columns] partial sums of the gains' gradients
 };
 
-// Upper bound of the backward's CTAs for these sizes (sizes its workspace).
-int norm_rope_bwd_ctas(long B, long N);
-// Chooses tile, tiles_per_b, n_tiles and ctas.
+// Floats of partial sums the backward may need for these sizes.
+size_t norm_rope_part_floats(long B, long N, long Hq, long Hk, long D);
+// Chooses the work split.
 void norm_rope_plan(NormRopeParams* p, bool backward);
 cudaError_t launch_norm_rope_fwd(const NormRopeParams& p, cudaStream_t s);
 cudaError_t launch_norm_rope_bwd(const NormRopeParams& p, cudaStream_t s);
