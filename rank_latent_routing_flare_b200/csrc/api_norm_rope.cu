@@ -74,7 +74,7 @@ flare_status fill(const flare_qk_norm_rope_args* a, bool backward, NormRopeParam
                 a->kr_stride, backward ? a->dK : a->Kr, backward ? a->dk_stride : a->kr_stride,
                 backward ? a->dk_gain : nullptr, backward);
   if (r != FLARE_OK) return r;
-  norm_rope_plan(p, backward);
+  norm_rope_plan(p);
   return FLARE_OK;
 }
 

@@ -8,8 +8,9 @@
 //   dx = r (w - x r^2 mean(w x)),  dg = sum over rows of u x r
 //
 // Bound by HBM: every row is read once and written once (backward: two reads
-// and one write).  A lane holds 8 elements (one 16-byte access), D / 8 lanes a
-// row, so the row's sums are a few shuffles and nothing is staged.  The input
+// and one write).  A lane holds 16 elements, D / 16 lanes a row, in two
+// 16-byte pieces chosen so that both members of a pair are the lane's own:
+// the rotation needs no exchange, and the row's sums are a few shuffles.  The input
 // usually is token-major (a slice of a projection) and the output head-major:
 // a warp takes a group of up to 64 / D heads of several tokens, so that both
 // sides move in pieces of 128 bytes or more.  It stays with its group: gains
@@ -30,8 +31,10 @@ namespace flare {
 namespace {
 
 constexpr int kMaxWarps = 8;
-constexpr int kWarpsPerSM = 24;   // resident at 80 registers a thread
+constexpr int kWarpsPerSM = 16;   // resident at 128 registers a thread
+constexpr int kTableBytes = 16384; // of one tile's angles, at most
 constexpr int kRedCols = 128;     // columns of a group: ht * D
+constexpr int kTablePad = 4;
 
 // Heads of a group: 64 / D (128 bytes of a token-major row), or the largest
 // power of two below that divides the head count.
@@ -47,9 +50,35 @@ __host__ __device__ inline int groups_of(int H, int D) { return H ? H / heads_pe
 template <int D, bool IL>
 __device__ __forceinline__ int table_width(int P) { return IL ? D / 2 : P; }
 
-// cos and sin of the tile's first `nvalid` tokens: cs[token][cos W | sin W].
+// Walks a CTA's tiles: range, range + ranges, ...
+struct Walk {
+  long tile;
+  int b, n0, ntok, nvalid;   // tokens n0 .. n0 + ntok of entry b, the first nvalid of them not padding
+  __device__ __forceinline__ void open(const NormRopeParams& p) {
+    ntok = nvalid = 0;
+    if (tile >= p.n_tiles) return;
+    b = static_cast<int>(tile / p.tiles_per_b);
+    n0 = static_cast<int>(tile - static_cast<long>(b) * p.tiles_per_b) * p.tile;
+    ntok = min(p.tile, p.N - n0);
+    nvalid = p.lengths == nullptr ? ntok : max(0, min(ntok, p.lengths[b] - n0));
+  }
+};
+
+// Positions of a tile's tokens into shared memory, asynchronously.
+__device__ __forceinline__ void copy_positions(const NormRopeParams& p, const Walk& w, float* dst) {
+  if (p.pos_kind != 0) {
+    const float* src = static_cast<const float*>(p.pos) + (static_cast<long>(w.b) * p.N + w.n0) * p.axes;
+    for (int i = threadIdx.x; i < w.nvalid * p.axes; i += blockDim.x)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst + i)), "l"(src + i) : "memory");
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void wait_positions() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// cos and sin of the tile's first `nvalid` tokens: cs[token][cos W | sin W | pad].
+// The padding puts the pieces that the tokens of a warp read on different banks.
 template <int D, bool IL>
-__device__ __forceinline__ void fill_angles(const NormRopeParams& p, int b, int n0, int nvalid, float* cs) {
+__device__ __forceinline__ void fill_angles(const NormRopeParams& p, const Walk& w, const float* pos, float* cs) {
   const int W = table_width<D, IL>(p.P);
   const int bits = W <= 1 ? 0 : 32 - __clz(W - 1);          // a thread keeps one pair
   const int q = threadIdx.x & ((1 << bits) - 1), step = blockDim.x >> bits, t0 = threadIdx.x >> bits;
@@ -58,128 +87,133 @@ __device__ __forceinline__ void fill_angles(const NormRopeParams& p, int b, int 
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     f[k] = k < p.axes && q < p.P ? static_cast<double>(p.freqs[k * p.P + q]) * 0.15915494309189533577 : 0.0;   // turns
-  for (int t = t0; t < nvalid; t += step) {
-    const int n = n0 + t;
+  for (int t = t0; t < w.nvalid; t += step) {
     double a;
     if (p.pos_kind == 2) {
-      const float* pos = static_cast<const float*>(p.pos) + (static_cast<long>(b) * p.N + n) * p.axes;
-      a = static_cast<double>(pos[0]) * f[0];
+      a = static_cast<double>(pos[t * p.axes]) * f[0];
 #pragma unroll
       for (int k = 1; k < 4; ++k)
-        if (k < p.axes) a = fma(static_cast<double>(pos[k]), f[k], a);
+        if (k < p.axes) a = fma(static_cast<double>(pos[t * p.axes + k]), f[k], a);
     } else {
-      a = static_cast<double>(p.pos_kind == 1 ? static_cast<const int*>(p.pos)[static_cast<long>(b) * p.N + n] : n) * f[0];
+      a = static_cast<double>(p.pos_kind == 1 ? __float_as_int(pos[t]) : w.n0 + t) * f[0];
     }
     a -= rint(a);
     float sn, cn;
     sincospif(2.0f * static_cast<float>(a), &sn, &cn);
-    cs[t * 2 * W + q] = cn;
-    cs[t * 2 * W + W + q] = sn;
+    cs[t * (2 * W + kTablePad) + q] = cn;
+    cs[t * (2 * W + kTablePad) + W + q] = sn;
   }
 }
 
-// 8 elements of a row as four fp32 pairs.
-struct Vec8 {
-  uint64_t v[4];
+// 16 elements of a row: two pieces of 8, each as four fp32 pairs.
+struct Vec16 {
+  uint64_t v[8];
 };
-__device__ __forceinline__ Vec8 unpack(const uint4& r) {
-  return Vec8{{f2_pack(bf16_lo(r.x), bf16_hi(r.x)), f2_pack(bf16_lo(r.y), bf16_hi(r.y)),
-               f2_pack(bf16_lo(r.z), bf16_hi(r.z)), f2_pack(bf16_lo(r.w), bf16_hi(r.w))}};
+__device__ __forceinline__ void unpack8(const uint4& r, uint64_t* v) {
+  v[0] = f2_pack(bf16_lo(r.x), bf16_hi(r.x));
+  v[1] = f2_pack(bf16_lo(r.y), bf16_hi(r.y));
+  v[2] = f2_pack(bf16_lo(r.z), bf16_hi(r.z));
+  v[3] = f2_pack(bf16_lo(r.w), bf16_hi(r.w));
 }
 __device__ __forceinline__ uint32_t round_pair(uint64_t v) {
   float lo, hi;
   f2_unpack(v, lo, hi);
   return pack_bf16x2(lo, hi);
 }
-__device__ __forceinline__ uint4 pack(const Vec8& x) {
-  return make_uint4(round_pair(x.v[0]), round_pair(x.v[1]), round_pair(x.v[2]), round_pair(x.v[3]));
+__device__ __forceinline__ uint4 pack8(const uint64_t* v) {
+  return make_uint4(round_pair(v[0]), round_pair(v[1]), round_pair(v[2]), round_pair(v[3]));
 }
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) { return f2_fma(a, b, f2_pack(-0.f, -0.f)); }
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t f2_dup(float a) { return f2_pack(a, a); }
-__device__ __forceinline__ Vec8 load_gain(const float* g) {
+__device__ __forceinline__ void load_gain8(const float* g, uint64_t* v) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(g)), b = __ldg(reinterpret_cast<const float4*>(g) + 1);
-  return Vec8{{f2_pack(a.x, a.y), f2_pack(a.z, a.w), f2_pack(b.x, b.y), f2_pack(b.z, b.w)}};
+  v[0] = f2_pack(a.x, a.y);
+  v[1] = f2_pack(a.z, a.w);
+  v[2] = f2_pack(b.x, b.y);
+  v[3] = f2_pack(b.z, b.w);
 }
-__device__ __forceinline__ float sum8(const Vec8& a, const Vec8& b) {   // <a, b>
-  uint64_t s = f2_mul(a.v[0], b.v[0]);
+__device__ __forceinline__ float dot16(const Vec16& a, const Vec16& b) {
+  uint64_t s = f2_mul(a.v[0], b.v[0]), u = f2_mul(a.v[4], b.v[4]);
 #pragma unroll
-  for (int i = 1; i < 4; ++i) s = f2_fma(a.v[i], b.v[i], s);
+  for (int i = 1; i < 4; ++i) {
+    s = f2_fma(a.v[i], b.v[i], s);
+    u = f2_fma(a.v[4 + i], b.v[4 + i], u);
+  }
   float lo, hi;
-  f2_unpack(s, lo, hi);
+  f2_unpack(f2_add(s, u), lo, hi);
   return lo + hi;
 }
-__device__ __forceinline__ uint4 shfl4(const uint4& v, int src) {
-  return make_uint4(__shfl_sync(~0u, v.x, src), __shfl_sync(~0u, v.y, src), __shfl_sync(~0u, v.z, src),
-                    __shfl_sync(~0u, v.w, src));
-}
 template <int D>
-__device__ __forceinline__ float row_sum(float v) {   // over the D / 8 lanes of a row
+__device__ __forceinline__ float row_sum(float v) {   // over the D / 16 lanes of a row
 #pragma unroll
-  for (int o = D / 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  for (int o = D / 32; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
 
-// The turn of a lane's 8 elements.  Half-split pairs: y = v cos + o sin, o the
-// pairs' other members (of lane src), already signed: -o for the first
-// members of a forward turn, +o for the second.  Interleaved pairs lie within
-// the lane; dir = 1 forward, -1 back.
-struct Turn {
-  int src, first;
-  bool turned;
-  float sign;
-};
+// A lane's place in its warp's group of rows: token t_in of tt, head h_in of
+// ht, and two pieces of 8 elements from e0 and e1: half-split pairs have one
+// member in each (pairs first .. first + 7), interleaved pairs lie within the
+// 16 consecutive elements (pairs first .. first + 7 too).
 template <int D, bool IL>
-__device__ __forceinline__ Turn lane_turn(int lane, int P) {
-  const int l = lane % (D / 8);
-  if (IL) return Turn{lane, 4 * l, 4 * l < P, 1.f};
-  const int ph = P / 8;
-  if (l < ph) return Turn{lane + ph, 8 * l, true, -1.f};
-  if (l < 2 * ph) return Turn{lane - ph, 8 * (l - ph), true, 1.f};
-  return Turn{lane, 0, false, 0.f};
-}
-template <bool IL>
-__device__ __forceinline__ void rotate(Vec8& v, const Vec8& o, const Turn& t, const float* cs, int W, float dir) {
-  const float4* c4 = reinterpret_cast<const float4*>(cs + t.first);
-  const float4* s4 = reinterpret_cast<const float4*>(cs + W + t.first);
-  if (IL) {
-    const float4 c = c4[0], s = s4[0];
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float a, b;
-      f2_unpack(v.v[i], a, b);
-      const float sn = dir * ss[i];
-      v.v[i] = f2_fma(f2_pack(-b, a), f2_dup(sn), f2_mul(v.v[i], f2_dup(cc[i])));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 c = c4[i], s = s4[i];
-      v.v[2 * i] = f2_fma(o.v[2 * i], f2_pack(s.x, s.y), f2_mul(v.v[2 * i], f2_pack(c.x, c.y)));
-      v.v[2 * i + 1] = f2_fma(o.v[2 * i + 1], f2_pack(s.z, s.w), f2_mul(v.v[2 * i + 1], f2_pack(c.z, c.w)));
-    }
-  }
-}
-
-// A lane's place in its warp's group: token t_in of tt, head h_in of ht, and
-// 8 elements from 8 l.
-template <int D>
 struct Place {
-  int ht, tt, h_in, t_in, l;
-  __device__ __forceinline__ Place(int H, int lane) {
-    constexpr int L = D / 8;
+  int ht, tt, h_in, t_in, e0, e1, first;
+  bool turned;
+  __device__ __forceinline__ Place(int H, int lane, int P) {
+    constexpr int L = D / 16;
     ht = heads_per_group(H, D);
     tt = (32 / L) / ht;
-    l = lane % L;
-    const int rr = lane / L;
+    const int l = lane % L, rr = lane / L;
     h_in = rr & (ht - 1);
     t_in = rr / ht;
+    if (IL) {
+      e0 = 16 * l;
+      e1 = e0 + 8;
+      first = 8 * l;
+      turned = first < P;
+    } else {
+      const int ph = P / 8;
+      turned = l < ph;
+      e0 = turned ? 8 * l : 16 * l;   // lanes behind the pairs' take the rest, 16 elements each: 2 P + 16 (l - ph)
+      e1 = turned ? P + 8 * l : e0 + 8;
+      first = 8 * l;
+    }
   }
 };
-
-__device__ __forceinline__ int valid_tokens(const NormRopeParams& p, int b, int n0, int ntok) {
-  if (p.lengths == nullptr) return ntok;
-  return max(0, min(ntok, p.lengths[b] - n0));
+// The pairs of a lane turned by the angles of a token (dir 1) or back (-1).
+template <bool IL>
+__device__ __forceinline__ void rotate(Vec16& x, const float* cs, int W, float dir) {
+  const float4* c4 = reinterpret_cast<const float4*>(cs);
+  const float4* s4 = reinterpret_cast<const float4*>(cs + W);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float4 c = c4[i], s = s4[i];
+    if (IL) {
+      const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint64_t& v = x.v[4 * i + k];
+        float a, b;
+        f2_unpack(v, a, b);
+        v = f2_fma(f2_pack(b, a), f2_pack(-dir * ss[k], dir * ss[k]), f2_mul(v, f2_dup(cc[k])));
+      }
+    } else {
+      const uint64_t cc[2] = {f2_pack(c.x, c.y), f2_pack(c.z, c.w)};
+      const uint64_t ss[2] = {f2_pack(dir * s.x, dir * s.y), f2_pack(dir * s.z, dir * s.w)};
+      const uint64_t ns[2] = {f2_pack(-dir * s.x, -dir * s.y), f2_pack(-dir * s.z, -dir * s.w)};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint64_t& a = x.v[2 * i + k];
+        uint64_t& b = x.v[4 + 2 * i + k];
+        const uint64_t ta = f2_fma(b, ns[k], f2_mul(a, cc[k]));
+        b = f2_fma(a, ss[k], f2_mul(b, cc[k]));
+        a = ta;
+      }
+    }
+  }
 }
 
 // This warp's group of the CTA and its share of a tile's tokens.
@@ -193,155 +227,32 @@ __device__ __forceinline__ Unit warp_unit(const NormRopeParams& p) {
   return g >= p.groups ? Unit{0, part, -1} : g < nq ? Unit{g, part, 0} : Unit{g - nq, part, 1};
 }
 
-template <int D, bool IL>
-__global__ void __launch_bounds__(32 * kMaxWarps, kWarpsPerSM / kMaxWarps) norm_rope_fwd_kernel(const __grid_constant__ NormRopeParams p) {
-  extern __shared__ __align__(16) float cs[];
-  constexpr int U = 4;   // rows in flight per lane
-  const int lane = threadIdx.x & 31;
-  const long tile = blockIdx.x / p.ctas_y;
-  const int b = static_cast<int>(tile / p.tiles_per_b);
-  const int n0 = static_cast<int>(tile - static_cast<long>(b) * p.tiles_per_b) * p.tile;
-  const int ntok = min(p.tile, p.N - n0), nvalid = valid_tokens(p, b, n0, ntok);
-  const Unit unit = warp_unit(p);
-  if (p.P > 0) {
-    fill_angles<D, IL>(p, b, n0, nvalid, cs);
-    __syncthreads();
-  }
-  if (unit.side < 0) return;
-  const NormRopeSide& s = p.side[unit.side];
-  const Place<D> at(s.H, lane);
-  const Turn turn = lane_turn<D, IL>(lane, p.P);
-  const int W = table_width<D, IL>(p.P), head = unit.group * at.ht + at.h_in;
-  const uint16_t* x0 = s.x + b * s.xs[0] + head * s.xs[1] + static_cast<long>(n0) * s.xs[2] + 8 * at.l;
-  uint16_t* y0 = s.y + b * s.ys[0] + head * s.ys[1] + static_cast<long>(n0) * s.ys[2] + 8 * at.l;
-  // the gain, and for half-split pairs the signed gain of the other members
-  Vec8 g, go;
-  const float* gp = s.gain + (s.gain_per_head ? static_cast<long>(head) * D : 0);
-  if (s.gain) g = load_gain(gp + 8 * at.l);
-  if (s.gain && !IL) go = load_gain(gp + 8 * (turn.src % (D / 8)));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (!s.gain) g.v[i] = go.v[i] = f2_dup(1.f);
-    if (!IL) go.v[i] = f2_mul(go.v[i], f2_dup(turn.sign));
-  }
-  const int step = p.parts * at.tt;   // tokens between a lane's rows
-  for (int t0 = unit.part * at.tt; t0 < ntok; t0 += U * step) {
-    uint4 raw[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int t = t0 + u * step + at.t_in;
-      raw[u] = make_uint4(0, 0, 0, 0);
-      if (t < nvalid) raw[u] = *reinterpret_cast<const uint4*>(x0 + t * s.xs[2]);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (t0 + u * step >= ntok) break;   // uniform over the warp
-      const int t = t0 + u * step + at.t_in;
-      Vec8 x = unpack(raw[u]), o;
-      const uint64_t r = f2_dup(rsqrtf(fmaf(row_sum<D>(sum8(x, x)), 1.0f / D, p.eps)));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x.v[i] = f2_mul(x.v[i], f2_mul(g.v[i], r));
-      if (!IL && p.P > 0) {
-        o = unpack(shfl4(raw[u], turn.src));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o.v[i] = f2_mul(o.v[i], f2_mul(go.v[i], r));
-      }
-      if (turn.turned && t < nvalid) rotate<IL>(x, o, turn, cs + t * 2 * W, W, 1.f);
-      if (t < ntok) *reinterpret_cast<uint4*>(y0 + t * s.ys[2]) = t < nvalid ? pack(x) : make_uint4(0, 0, 0, 0);
-    }
-  }
-}
-
 // Columns of a side's gain gradient in a CTA's partial row.
 __host__ __device__ inline int gain_cols(const NormRopeSide& s, int D) {
   return s.dgain ? (s.gain_per_head ? s.H * D : D) : 0;
 }
 
+// A CTA's partial row of the gains' gradients: the lanes of one head, then the
+// warps, in a fixed order.
 template <int D, bool IL>
-__global__ void __launch_bounds__(32 * kMaxWarps, kWarpsPerSM / kMaxWarps) norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
-  extern __shared__ __align__(16) float cs[];
-  __shared__ float red[kMaxWarps][kRedCols];
-  constexpr int U = 2;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int range = static_cast<int>(blockIdx.x / p.ctas_y);
-  const Unit unit = warp_unit(p);
-  const NormRopeSide& s = p.side[max(unit.side, 0)];
-  const Place<D> at(max(s.H, 1), lane);
-  const Turn turn = lane_turn<D, IL>(lane, p.P);
-  const int W = table_width<D, IL>(p.P), head = unit.group * at.ht + at.h_in;
-  Vec8 g, dg;
-  if (s.gain) g = load_gain(s.gain + (s.gain_per_head ? static_cast<long>(head) * D : 0) + 8 * at.l);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (!s.gain) g.v[i] = f2_dup(1.f);
-    dg.v[i] = f2_dup(0.f);
-  }
-  const uint64_t back = f2_dup(-turn.sign);
-  for (long tile = range; tile < p.n_tiles; tile += p.ranges) {
-    const int b = static_cast<int>(tile / p.tiles_per_b);
-    const int n0 = static_cast<int>(tile - static_cast<long>(b) * p.tiles_per_b) * p.tile;
-    const int ntok = min(p.tile, p.N - n0), nvalid = valid_tokens(p, b, n0, ntok);
-    if (p.P > 0) {
-      __syncthreads();   // the previous tile's angles are read
-      fill_angles<D, IL>(p, b, n0, nvalid, cs);
-      __syncthreads();
-    }
-    if (unit.side < 0) continue;
-    const uint16_t* x0 = s.x + b * s.xs[0] + head * s.xs[1] + static_cast<long>(n0) * s.xs[2] + 8 * at.l;
-    const uint16_t* d0 = s.dy + b * s.ds[0] + head * s.ds[1] + static_cast<long>(n0) * s.ds[2] + 8 * at.l;
-    uint16_t* y0 = s.y + b * s.ys[0] + head * s.ys[1] + static_cast<long>(n0) * s.ys[2] + 8 * at.l;
-    const int step = p.parts * at.tt;
-    for (int t0 = unit.part * at.tt; t0 < ntok; t0 += U * step) {
-      uint4 rx[U], rd[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = t0 + u * step + at.t_in;
-        rx[u] = rd[u] = make_uint4(0, 0, 0, 0);
-        if (t < nvalid) {
-          rx[u] = *reinterpret_cast<const uint4*>(x0 + t * s.xs[2]);
-          rd[u] = *reinterpret_cast<const uint4*>(d0 + t * s.ds[2]);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (t0 + u * step >= ntok) break;   // uniform over the warp
-        const int t = t0 + u * step + at.t_in;
-        Vec8 x = unpack(rx[u]), v = unpack(rd[u]), o;
-        if (!IL && p.P > 0) {
-          o = unpack(shfl4(rd[u], turn.src));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o.v[i] = f2_mul(o.v[i], back);
-        }
-        if (turn.turned && t < nvalid) rotate<IL>(v, o, turn, cs + t * 2 * W, W, -1.f);
-        const float sq = row_sum<D>(sum8(x, x));
-        Vec8 w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w.v[i] = f2_mul(v.v[i], g.v[i]);
-        const float wx = row_sum<D>(sum8(w, x));
-        const float r = rsqrtf(fmaf(sq, 1.0f / D, p.eps));
-        const uint64_t r2 = f2_dup(r), k2 = f2_dup(-r * r * wx * (1.0f / D));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dg.v[i] = f2_fma(v.v[i], f2_mul(x.v[i], r2), dg.v[i]);
-          w.v[i] = f2_mul(r2, f2_fma(x.v[i], k2, w.v[i]));
-        }
-        if (t < ntok) *reinterpret_cast<uint4*>(y0 + t * s.ys[2]) = t < nvalid ? pack(w) : make_uint4(0, 0, 0, 0);
-      }
-    }
-  }
+__device__ __forceinline__ void gain_row(const NormRopeParams& p, float (*red)[kRedCols], const Place<D, IL>& at, const Vec16& dg) {
+  const int warp = threadIdx.x >> 5;
   const int cq = gain_cols(p.side[0], D), cols = cq + gain_cols(p.side[1], D);
   if (cols == 0) return;
-  // the CTA's partial row: lanes of one head, then the warps, in a fixed order
-  float f[8];
+  __syncthreads();   // red lies over the tables
+  float f[16];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f2_unpack(dg.v[i], f[2 * i], f[2 * i + 1]);
-  for (int o = at.ht * (D / 8); o < 32; o <<= 1) {
+  for (int i = 0; i < 8; ++i) f2_unpack(dg.v[i], f[2 * i], f[2 * i + 1]);
+  for (int o = at.ht * (D / 16); o < 32; o <<= 1) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] += __shfl_xor_sync(~0u, f[e], o);
+    for (int e = 0; e < 16; ++e) f[e] += __shfl_xor_sync(~0u, f[e], o);
   }
   if (at.t_in == 0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) red[warp][at.h_in * D + 8 * at.l + e] = f[e];
+    for (int e = 0; e < 8; ++e) {
+      red[warp][at.h_in * D + at.e0 + e] = f[e];
+      red[warp][at.h_in * D + at.e1 + e] = f[8 + e];
+    }
   }
   __syncthreads();
   float* row = p.part + static_cast<long>(blockIdx.x) * cols;
@@ -370,6 +281,148 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kWarpsPerSM / kMaxWarps) norm_
       }
     }
   }
+}
+
+// Both directions.  Positions come to shared memory two tiles ahead; a tile's
+// first rows are requested before its angles are computed.  Two angle tables and two position buffers:
+// one barrier a tile.
+template <int D, bool IL, bool BWD>
+__global__ void __launch_bounds__(32 * kMaxWarps, kWarpsPerSM / kMaxWarps) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+  extern __shared__ __align__(16) float smem[];
+  constexpr int U = BWD ? 1 : 2;   // rows a lane requests at once
+  const int lane = threadIdx.x & 31;
+  const int range = static_cast<int>(blockIdx.x / p.ctas_y);
+  const Unit unit = warp_unit(p);
+  const bool active = unit.side >= 0;
+  const NormRopeSide& s = p.side[max(unit.side, 0)];
+  const Place<D, IL> at(max(s.H, 1), lane, p.P);
+  const int W = table_width<D, IL>(p.P), row = 2 * W + kTablePad, table = p.tile * row;
+  const int head = unit.group * at.ht + at.h_in;
+  const int step = p.parts * at.tt, t_first = unit.part * at.tt + at.t_in;
+  const uint16_t* x0 = s.x + head * s.xs[1] + at.e0;
+  const uint16_t* d0 = BWD ? s.dy + head * s.ds[1] + at.e0 : nullptr;
+  uint16_t* y0 = s.y + head * s.ys[1] + at.e0;
+  const int other = at.e1 - at.e0;
+
+  Vec16 g, dg;
+  const float* gp = s.gain + (s.gain_per_head ? static_cast<long>(head) * D : 0);
+  if (s.gain) {
+    load_gain8(gp + at.e0, g.v);
+    load_gain8(gp + at.e1, g.v + 4);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (!s.gain) g.v[i] = f2_dup(1.f);
+    dg.v[i] = f2_dup(0.f);
+  }
+
+  float* pos = smem + 2 * table;
+  const int pos_floats = p.tile * p.axes;
+  uint4 rx[U][2], rd[U][2];
+  Walk w, next;
+  const uint16_t *x, *d;
+  auto fetch = [&](const Walk& at_tile, int t0) {   // a lane's next U rows
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + u * step;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) rx[u][i] = rd[u][i] = make_uint4(0, 0, 0, 0);
+      if (active && t < at_tile.nvalid) {
+        rx[u][0] = *reinterpret_cast<const uint4*>(x + t * s.xs[2]);
+        rx[u][1] = *reinterpret_cast<const uint4*>(x + t * s.xs[2] + other);
+        if (BWD) {
+          rd[u][0] = *reinterpret_cast<const uint4*>(d + t * s.ds[2]);
+          rd[u][1] = *reinterpret_cast<const uint4*>(d + t * s.ds[2] + other);
+        }
+      }
+    }
+  };
+  auto begin = [&](const Walk& at_tile) {           // a tile's first rows
+    if (at_tile.ntok == 0) return;
+    x = x0 + at_tile.b * s.xs[0] + static_cast<long>(at_tile.n0) * s.xs[2];
+    if (BWD) d = d0 + at_tile.b * s.ds[0] + static_cast<long>(at_tile.n0) * s.ds[2];
+    fetch(at_tile, t_first);
+  };
+  auto copy = [&](int k, Walk at_tile) {            // positions of the CTA's k-th tile
+    copy_positions(p, at_tile, pos + (k & 1) * pos_floats);
+  };
+  auto after = [&](Walk at_tile) {
+    at_tile.tile += p.ranges;
+    at_tile.open(p);
+    return at_tile;
+  };
+  next.tile = range;
+  next.open(p);
+  begin(next);
+  if (p.P > 0) {
+    copy(0, next);
+    copy(1, after(next));
+    wait_positions();
+    __syncthreads();
+    fill_angles<D, IL>(p, next, pos, smem);
+  }
+  for (int k = 0; next.ntok > 0; ++k) {
+    w = next;
+    next = after(w);
+    const float* cs = smem + (k & 1) * table;
+    if (p.P > 0) {
+      // behind the barrier: this tile's angles, the next tile's positions, and
+      // every warp done with the tile before
+      wait_positions();
+      __syncthreads();
+      copy(k, after(next));   // k + 2
+    }
+    uint16_t* y = y0 + w.b * s.ys[0] + static_cast<long>(w.n0) * s.ys[2];
+    for (int t0 = t_first; active && t0 - at.t_in < w.ntok; t0 += U * step) {
+      Vec16 v[U], u[BWD ? U : 1];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        unpack8(rx[i][0], v[i].v);
+        unpack8(rx[i][1], v[i].v + 4);
+        if constexpr (BWD) {
+          unpack8(rd[i][0], u[i].v);
+          unpack8(rd[i][1], u[i].v + 4);
+        }
+      }
+      if (t0 + U * step - at.t_in < w.ntok) fetch(w, t0 + U * step); else begin(next);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int t = t0 + i * step;
+        if (t - at.t_in >= w.ntok) break;   // uniform over the warp
+        Vec16& x16 = v[i];
+        const float r = rsqrtf(fmaf(row_sum<D>(dot16(x16, x16)), 1.0f / D, p.eps));
+        const uint64_t r2 = f2_dup(r);
+        if constexpr (!BWD) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x16.v[e] = f2_mul(f2_mul(x16.v[e], r2), g.v[e]);
+          if (at.turned && t < w.nvalid) rotate<IL>(x16, cs + t * row + at.first, W, 1.f);
+        } else {
+          Vec16& u16 = u[i];
+          if (at.turned && t < w.nvalid) rotate<IL>(u16, cs + t * row + at.first, W, -1.f);
+          uint64_t sum2 = f2_dup(0.f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum2 = f2_fma(f2_mul(u16.v[e], g.v[e]), x16.v[e], sum2);   // <w, x>
+          float s0, s1;
+          f2_unpack(sum2, s0, s1);
+          const uint64_t k2 = f2_dup(-r * r * row_sum<D>(s0 + s1) * (1.0f / D));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            dg.v[e] = f2_fma(u16.v[e], f2_mul(x16.v[e], r2), dg.v[e]);
+            x16.v[e] = f2_mul(r2, f2_fma(x16.v[e], k2, f2_mul(u16.v[e], g.v[e])));
+          }
+        }
+        if (t < w.ntok) {
+          const bool live = t < w.nvalid;
+          uint16_t* dst = y + t * s.ys[2];
+          *reinterpret_cast<uint4*>(dst) = live ? pack8(x16.v) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(dst + other) = live ? pack8(x16.v + 4) : make_uint4(0, 0, 0, 0);
+        }
+      }
+    }
+    if (t_first - at.t_in >= w.ntok) begin(next);   // a share without tokens in a short tile
+    if (p.P > 0) fill_angles<D, IL>(p, next, pos + ((k + 1) & 1) * pos_floats, smem + ((k + 1) & 1) * table);
+  }
+  if constexpr (BWD) gain_row<D, IL>(p, reinterpret_cast<float(*)[kRedCols]>(smem), at, dg);
 }
 
 // Sum of the CTAs' partial rows, in a fixed order: 32 columns a block, the
@@ -410,18 +463,36 @@ cudaError_t by_dim(int D, int interleaved, F&& f) {
   return cudaErrorInvalidValue;
 }
 
-size_t table_bytes(const NormRopeParams& p) {
-  return p.P == 0 ? 0 : static_cast<size_t>(p.tile) * 2 * (p.interleaved ? p.D / 2 : p.P) * sizeof(float);
+// CTAs over the tiles in one wave.
+long range_slots(const NormRopeParams& p) {
+  return std::max(1L, static_cast<long>(kNumSM) * (kWarpsPerSM / (p.cta_groups * p.parts)) / p.ctas_y);
+}
+
+// Two tables of angles and two buffers of positions; in the backward the warps' gradient sums lie over them.
+size_t smem_bytes(const NormRopeParams& p, bool backward) {
+  const size_t row = 2 * (p.interleaved ? p.D / 2 : p.P) + kTablePad;
+  const size_t tables = p.P == 0 ? 0 : 2 * static_cast<size_t>(p.tile) * (row + p.axes) * sizeof(float);
+  return std::max(tables, backward ? kMaxWarps * kRedCols * sizeof(float) : 0);
+}
+
+template <bool BWD>
+cudaError_t launch(const NormRopeParams& p, cudaStream_t s) {
+  const size_t smem = smem_bytes(p, BWD);   // at most 2 (kTableBytes + 8 floats a token)
+  return by_dim(p.D, p.interleaved, [&](auto d, auto il) {
+    norm_rope_kernel<decltype(d)::value, decltype(il)::value, BWD>
+        <<<static_cast<unsigned>(static_cast<long>(p.ranges) * p.ctas_y), 32 * p.cta_groups * p.parts, smem, s>>>(p);
+    return cudaGetLastError();
+  });
 }
 
 }  // namespace
 
 // Work split.  Warps: up to 8 groups a CTA; where there are fewer, `parts`
-// warps share a group's tokens.  Tile: 8 rows a lane or more and 4 angles a
-// thread, at most 16 KB of angles; halved while the tiles do not give every SM
-// two CTAs.  The backward's CTAs stay for all of their tiles: one wave of
-// them, and the tile size (of three) that leaves the least of it idle.
-void norm_rope_plan(NormRopeParams* p, bool backward) {
+// warps share a group's tokens.  One wave of CTAs, each with every ranges-th
+// tile.  Tile: 8 rows a lane or more, 4 angles a thread and kTableBytes of
+// angles at most; halved while the tiles do not give every SM two CTAs, and
+// then the size (of three) that leaves the least of the wave idle.
+void norm_rope_plan(NormRopeParams* p) {
   p->groups = groups_of(p->side[0].H, p->D) + groups_of(p->side[1].H, p->D);
   p->ctas_y = (p->groups + kMaxWarps - 1) / kMaxWarps;
   p->cta_groups = (p->groups + p->ctas_y - 1) / p->ctas_y;
@@ -429,29 +500,26 @@ void norm_rope_plan(NormRopeParams* p, bool backward) {
   const int warps = p->cta_groups * p->parts;
   int tt = 1;
   for (const NormRopeSide& s : p->side)
-    if (s.H) tt = std::max(tt, 256 / p->D / heads_per_group(s.H, p->D));
+    if (s.H) tt = std::max(tt, 512 / p->D / heads_per_group(s.H, p->D));
   const long width = p->interleaved ? p->D / 2 : p->P;
   long t = 8L * tt * p->parts;
   while (t * width < 4 * 32 * warps && width > 0) t *= 2;
-  while (t > 1 && t * width * 8 > 16384) t /= 2;
+  while (t > 1 && t * width * 8 > kTableBytes) t /= 2;
   auto tiles = [&](long tile) { return static_cast<long>(p->B) * ((p->N + tile - 1) / tile); };
   while (t > 1 && tiles(t) * p->ctas_y < 2 * kNumSM) t /= 2;
-  if (backward) {
-    const long slots = std::max(1L, static_cast<long>(kNumSM) * (kWarpsPerSM / warps) / p->ctas_y);
-    long best = t, best_cost = -1;
-    for (long c = t, k = 0; c >= 1 && k < 3; c /= 2, ++k) {
-      const long cost = (tiles(c) + slots - 1) / slots * (c + tt * p->parts);
-      if (best_cost < 0 || cost < best_cost) {
-        best_cost = cost;
-        best = c;
-      }
+  const long slots = range_slots(*p);
+  long best = t, best_cost = -1;
+  for (long c = t, k = 0; c >= 1 && k < 3; c /= 2, ++k) {
+    const long cost = (tiles(c) + slots - 1) / slots * (c + tt * p->parts);
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      best = c;
     }
-    t = best;
-    p->ranges = static_cast<int>(std::min(slots, tiles(t)));
   }
-  p->tile = static_cast<int>(t);
-  p->tiles_per_b = static_cast<int>((p->N + t - 1) / t);
-  p->n_tiles = tiles(t);
+  p->tile = static_cast<int>(best);
+  p->tiles_per_b = static_cast<int>((p->N + best - 1) / best);
+  p->n_tiles = tiles(best);
+  p->ranges = static_cast<int>(std::min(slots, p->n_tiles));
 }
 
 size_t norm_rope_part_floats(long B, long N, long Hq, long Hk, long D) {
@@ -461,26 +529,14 @@ size_t norm_rope_part_floats(long B, long N, long Hq, long Hk, long D) {
   p.D = static_cast<int>(D);
   p.side[0].H = static_cast<int>(Hq);
   p.side[1].H = static_cast<int>(Hk);
-  // a range has at least one token
-  norm_rope_plan(&p, true);
-  const long slots = std::max(1L, static_cast<long>(kNumSM) * (kWarpsPerSM / (p.cta_groups * p.parts)) / p.ctas_y);
-  return static_cast<size_t>(std::min(slots, B * N)) * p.ctas_y * (Hq + Hk) * D;
+  norm_rope_plan(&p);
+  return static_cast<size_t>(std::min(range_slots(p), B * N)) * p.ctas_y * (Hq + Hk) * D;   // a tile has a token at least
 }
 
-cudaError_t launch_norm_rope_fwd(const NormRopeParams& p, cudaStream_t s) {
-  return by_dim(p.D, p.interleaved, [&](auto d, auto il) {
-    norm_rope_fwd_kernel<decltype(d)::value, decltype(il)::value>
-        <<<static_cast<unsigned>(p.n_tiles * p.ctas_y), 32 * p.cta_groups * p.parts, table_bytes(p), s>>>(p);
-    return cudaGetLastError();
-  });
-}
+cudaError_t launch_norm_rope_fwd(const NormRopeParams& p, cudaStream_t s) { return launch<false>(p, s); }
 
 cudaError_t launch_norm_rope_bwd(const NormRopeParams& p, cudaStream_t s) {
-  const cudaError_t e = by_dim(p.D, p.interleaved, [&](auto d, auto il) {
-    norm_rope_bwd_kernel<decltype(d)::value, decltype(il)::value>
-        <<<static_cast<unsigned>(static_cast<long>(p.ranges) * p.ctas_y), 32 * p.cta_groups * p.parts, table_bytes(p), s>>>(p);
-    return cudaGetLastError();
-  });
+  const cudaError_t e = launch<true>(p, s);
   const int cols = gain_cols(p.side[0], p.D) + gain_cols(p.side[1], p.D);
   if (e != cudaSuccess || cols == 0) return e;
   gain_sum_kernel<<<(cols + 31) / 32, dim3(32, 32), 0, s>>>(p);

@@ -35,14 +35,14 @@ struct NormRopeParams {
   int tile;             // tokens per tile
   int tiles_per_b;
   long n_tiles;         // B * tiles_per_b
-  int ranges;           // backward: CTAs over the tiles, each taking every ranges-th
+  int ranges;           // CTAs over the tiles, each taking every ranges-th
   float* part;          // backward: [ranges][ctas_y][gain columns] partial sums of the gains' gradients
 };
 
 // Floats of partial sums the backward may need for these sizes.
 size_t norm_rope_part_floats(long B, long N, long Hq, long Hk, long D);
 // Chooses the work split.
-void norm_rope_plan(NormRopeParams* p, bool backward);
+void norm_rope_plan(NormRopeParams* p);
 cudaError_t launch_norm_rope_fwd(const NormRopeParams& p, cudaStream_t s);
 cudaError_t launch_norm_rope_bwd(const NormRopeParams& p, cudaStream_t s);
 
