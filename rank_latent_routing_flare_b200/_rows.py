@@ -1,77 +1,99 @@
 """Helpers of the operators of include/flare_ops.h: checks of [B, H, N, D]
-tensors of rows and the packing of argument structs (every member 8 bytes)."""
+tensors of rows and the packing of argument structs (every member 8 bytes).
+
+A call on a few rows takes a few microseconds on the GPU, so the checks read
+each tensor's properties once and hand back what the struct needs.
+"""
 from __future__ import annotations
+
+import functools
 
 import torch
 
 from . import _binding as b
 
 ROW_WIDTHS = (16, 32, 64, 128)
+NO_ROWS = (0, 0, 0, 0)
+_bf16 = torch.bfloat16
 
 
-def check_rows(name, t, shape, output=False):
-    """bf16 CUDA tensor of that shape, dense along D, rows on 16-byte boundaries."""
+def rows(t):
+    """Pointer and the three strides of a tensor of rows, as the argument structs hold them."""
+    return (t.data_ptr(), *t.stride()[:3])
+
+
+def check_rows(name, t, shape, dev, output=False):
+    """Checks a bf16 tensor of that shape on GPU `dev`, dense along D, its rows
+    on 16-byte boundaries; returns its pointer and strides."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if t.dtype is not _bf16:
+        raise TypeError(f"{name} must be {_bf16}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    p, (sb, sh, sn, sd) = t.data_ptr(), t.stride()
+    if sd != 1 and shape[3] > 1:
+        raise ValueError(f"{name} must be dense along its last dimension")
+    if p & 15 or (sb | sh | sn) & 7:
+        if p & 15 or any(s & 7 for s, n in zip((sb, sh, sn), shape) if n > 1):
+            raise ValueError(f"{name}: every row must start on a 16-byte boundary (strides {t.stride()})")
+    if output and not (sb and sh and sn) and any(s == 0 for s, n in zip((sb, sh, sn), shape) if n > 1):
+        raise ValueError(f"{name} is written and must not be an expanded view")
+    return p, sb, sh, sn
+
+
+def check_small(name, t, dtype, shape, dev) -> int:
+    """Checks an optional contiguous tensor on GPU `dev` (shape None: any); returns its pointer."""
+    if t is None:
+        return 0
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    sb, sh, sn, sd = t.stride()
-    if sd != 1:
-        raise ValueError(f"{name} must be dense along its last dimension")
-    if t.data_ptr() & 15 or any(s & 7 for s, n in zip((sb, sh, sn), shape) if n > 1):
-        raise ValueError(f"{name}: every row must start on a 16-byte boundary (strides {t.stride()})")
-    if output and any(s == 0 for s, n in zip((sb, sh, sn), shape) if n > 1):
-        raise ValueError(f"{name} is written and must not be an expanded view")
-
-
-def check_small(name, t, dtype, shape, device):
-    """Optional contiguous tensor on the operator's device."""
-    if t is None:
-        return
-    b._check_dev(name, t, dtype, shape)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-
-
-def same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
 
-def rows(t):
-    """Pointer and the three strides of a tensor of rows, as the argument structs hold them."""
-    if t is None:
-        return 0, 0, 0, 0
-    s = t.stride()
-    return t.data_ptr(), s[0], s[1], s[2]
+@functools.lru_cache(maxsize=None)
+def entry(name):
+    """Entry point of the library."""
+    return getattr(b.load_library(), name)
 
 
-def call(fn, where, device, stream, *args):
-    """fn(*args, stream) with `device` current; raises FlareError on a status other than OK."""
+def call(name, where, dev, stream, *args):
+    """The entry point called with GPU `dev` current, on `stream` (None: the
+    current one); raises FlareError on a status other than OK."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, stream.cuda_stream)
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on cuda:{dev}")
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, stream.cuda_stream)
+        s = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        st = entry(name)(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = entry(name)(*args, s)
     if st != 0:
         raise b.FlareError(st, where)
 
 
-def workspace(ws, nbytes, device):
+def workspace(ws, nbytes, like):
+    """The caller's workspace, checked, or a new one."""
     if ws is None:
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    check_small("workspace", ws, torch.uint8, None, device)
+        return torch.empty(nbytes if nbytes > 256 else 256, dtype=torch.uint8, device=like.device)
+    check_small("workspace", ws, torch.uint8, None, like.get_device())
     if ws.numel() < nbytes:
         raise ValueError(f"workspace has {ws.numel()} bytes, needs {nbytes}")
     return ws

@@ -8,54 +8,51 @@ marshalling only: the kernels are behind include/flare_ops.h.
 """
 from __future__ import annotations
 
+import functools
 import struct
 
 import torch
 
 from . import _binding as b
-from ._rows import ROW_WIDTHS, call, check_rows, check_small, ptr, rows, same_device, workspace as _ws
+from ._rows import NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, entry, ptr, rows, workspace as _ws
 
 # flare_attention_args
 _ARGS = struct.Struct("=7q2d12q6q4qq4q12q")
-_NONE4 = (0, 0, 0, 0)
+_f32, _i32 = torch.float32, torch.int32
 
 
+@functools.lru_cache(maxsize=4096)
 def flare_attention_workspace_bytes(B: int, Hq: int, Hk: int, Nq: int, Nk: int, D: int, backward: bool = False) -> int:
-    return int(b.load_library().flare_attention_workspace_bytes(B, Hq, Hk, Nq, Nk, D, int(backward)))
+    return int(entry("flare_attention_workspace_bytes")(B, Hq, Hk, Nq, Nk, D, int(backward)))
 
 
-def _check(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal):
-    if any(t.dim() != 4 for t in (Q, K, V)):
+def _head(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap, check):
+    """The inputs' part of the argument struct, in its order, and the sizes with the device index."""
+    if Q.dim() != 4 or K.dim() != 4 or V.dim() != 4:
         raise ValueError("Q, K and V are [B, H, N, D]")
     B, Hq, Nq, D = Q.shape
     Hk, Nk = K.shape[1:3]
-    if D not in ROW_WIDTHS:
-        raise ValueError(f"D is {D}, expected one of {ROW_WIDTHS}")
-    if Hk == 0 or Hq % Hk:
-        raise ValueError(f"{Hq} query heads are not a multiple of {Hk} key heads")
-    check_rows("Q", Q, (B, Hq, Nq, D))
-    check_rows("K", K, (B, Hk, Nk, D))
-    check_rows("V", V, (B, Hk, Nk, D))
-    dev = Q.device
-    same_device(dev, K=K, V=V)
-    for name, t in (("lengths", lengths), ("q_lengths", q_lengths), ("q_offsets", q_offsets), ("prefix", prefix)):
-        if t is not None:
-            check_small(name, t, torch.int32, (B,), dev)
-    if documents is not None:
-        check_small("documents", documents, torch.int32, (B, Nk), dev)
-    if slopes is not None:
-        check_small("slopes", slopes, torch.float32, (Hq,), dev)
-    if prefix is not None and not causal:
-        raise ValueError("prefix goes with causal=True")
-
-
-def _pack(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap, Y, L, back=None):
-    B, Hq, Nq, D = Q.shape
-    Hk, Nk = K.shape[1:3]
-    dY, dQ, dK, dV = (_NONE4,) * 4 if back is None else map(rows, back)
-    return _ARGS.pack(B, Hq, Hk, Nq, Nk, D, bool(causal), scale, cap, *rows(Q), *rows(K), *rows(V), ptr(lengths),
-                      ptr(q_lengths), ptr(q_offsets), ptr(documents), ptr(prefix), ptr(slopes), *rows(Y), ptr(L), *dY,
-                      *dQ, *dK, *dV)
+    dev = Q.get_device()
+    if check:
+        if not Q.is_cuda:
+            raise TypeError("Q must be a CUDA tensor")
+        if D not in ROW_WIDTHS:
+            raise ValueError(f"D is {D}, expected one of {ROW_WIDTHS}")
+        if Hk == 0 or Hq % Hk:
+            raise ValueError(f"{Hq} query heads are not a multiple of {Hk} key heads")
+        q = check_rows("Q", Q, (B, Hq, Nq, D), dev)
+        k = check_rows("K", K, (B, Hk, Nk, D), dev)
+        v = check_rows("V", V, (B, Hk, Nk, D), dev)
+        small = (check_small("lengths", lengths, _i32, (B,), dev), check_small("q_lengths", q_lengths, _i32, (B,), dev),
+                 check_small("q_offsets", q_offsets, _i32, (B,), dev),
+                 check_small("documents", documents, _i32, (B, Nk), dev),
+                 check_small("prefix", prefix, _i32, (B,), dev), check_small("slopes", slopes, _f32, (Hq,), dev))
+        if prefix is not None and not causal:
+            raise ValueError("prefix goes with causal=True")
+    else:
+        q, k, v = rows(Q), rows(K), rows(V)
+        small = (ptr(lengths), ptr(q_lengths), ptr(q_offsets), ptr(documents), ptr(prefix), ptr(slopes))
+    return (B, Hq, Hk, Nq, Nk, D, bool(causal), scale, cap, *q, *k, *v, *small), (B, Hq, Hk, Nq, Nk, D), dev
 
 
 def _device_check(device_check, ws, stream, where):
@@ -65,20 +62,25 @@ def _device_check(device_check, ws, stream, where):
             raise b.FlareError(st, where + " (device status)")
 
 
+def _output(name, t, like, dev, check):
+    """An output of `like`'s shape, new unless given, and its pointer and strides."""
+    if t is None:
+        t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    elif check:
+        return t, check_rows(name, t, like.shape, dev, output=True)
+    return t, rows(t)
+
+
 def _forward(where, Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap, Y, L,
              workspace, stream, check, device_check):
+    head, sizes, dev = _head(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap,
+                             check)
+    Y, y = _output("Y", Y, Q, dev, check)
     if check:
-        _check(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal)
-        if Y is not None:
-            check_rows("Y", Y, tuple(Q.shape), output=True)
-        check_small("L", L, torch.float32, tuple(Q.shape[:3]), Q.device)
-    dev = Q.device
-    if Y is None:
-        Y = torch.empty(Q.shape, dtype=torch.bfloat16, device=dev)
-    B, Hq, Nq, D = Q.shape
-    ws = _ws(workspace, flare_attention_workspace_bytes(B, Hq, K.shape[1], Nq, K.shape[2], D), dev)
-    args = _pack(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap, Y, L)
-    call(b.load_library().flare_attention_fwd, where, dev, stream, args, ws.data_ptr(), ws.numel())
+        check_small("L", L, _f32, Q.shape[:3], dev)
+    ws = _ws(workspace, flare_attention_workspace_bytes(*sizes), Q)
+    args = _ARGS.pack(*head, *y, ptr(L), *NO_ROWS, *NO_ROWS, *NO_ROWS, *NO_ROWS)
+    call("flare_attention_fwd", where, dev, stream, args, ws.data_ptr(), ws.numel())
     _device_check(device_check, ws, stream, where)
     return Y
 
@@ -121,27 +123,21 @@ def flare_attention_bwd(Q, K, V, Y, L, dY, lengths=None, q_lengths=None, q_offse
     """Gradients (dQ, dK, dV), bf16, given dY and the forward's Y and L (same
     inputs, masks, scale and cap).  dK and dV are summed over the query heads of
     a key head.  dQ, dK and dV may be preallocated strided views."""
+    head, sizes, dev = _head(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap,
+                             check)
+    if L is None:
+        raise ValueError("L is the forward's log-sum-exps")
     if check:
-        _check(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal)
-        for name, t in (("Y", Y), ("dY", dY)):
-            check_rows(name, t, tuple(Q.shape))
-            same_device(Q.device, **{name: t})
-        if L is None:
-            raise ValueError("L is the forward's log-sum-exps")
-        check_small("L", L, torch.float32, tuple(Q.shape[:3]), Q.device)
-        for name, t, x in (("dQ", dQ, Q), ("dK", dK, K), ("dV", dV, K)):
-            if t is not None:
-                check_rows(name, t, tuple(x.shape), output=True)
-                same_device(Q.device, **{name: t})
-    dev = Q.device
-    dQ = torch.empty(Q.shape, dtype=torch.bfloat16, device=dev) if dQ is None else dQ
-    dK = torch.empty(K.shape, dtype=torch.bfloat16, device=dev) if dK is None else dK
-    dV = torch.empty(K.shape, dtype=torch.bfloat16, device=dev) if dV is None else dV
-    B, Hq, Nq, D = Q.shape
-    ws = _ws(workspace, flare_attention_workspace_bytes(B, Hq, K.shape[1], Nq, K.shape[2], D, backward=True), dev)
-    args = _pack(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap, Y, L,
-                 (dY, dQ, dK, dV))
-    call(b.load_library().flare_attention_bwd, "flare_attention_bwd", dev, stream, args, ws.data_ptr(), ws.numel())
+        y, dy = check_rows("Y", Y, Q.shape, dev), check_rows("dY", dY, Q.shape, dev)
+        check_small("L", L, _f32, Q.shape[:3], dev)
+    else:
+        y, dy = rows(Y), rows(dY)
+    dQ, dq = _output("dQ", dQ, Q, dev, check)
+    dK, dk = _output("dK", dK, K, dev, check)
+    dV, dv = _output("dV", dV, K, dev, check)
+    ws = _ws(workspace, flare_attention_workspace_bytes(*sizes, backward=True), Q)
+    args = _ARGS.pack(*head, *y, L.data_ptr(), *dy, *dq, *dk, *dv)
+    call("flare_attention_bwd", "flare_attention_bwd", dev, stream, args, ws.data_ptr(), ws.numel())
     _device_check(device_check, ws, stream, "flare_attention_bwd")
     return dQ, dK, dV
 

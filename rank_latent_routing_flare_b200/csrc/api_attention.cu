@@ -51,7 +51,7 @@ AttnPlan make_attn_plan(int64_t B, int64_t Hq, int64_t Hk, int64_t Nq, int64_t N
     // one CTA per 256 rows of a head; where those leave half of the GPU idle,
     // the keys are split until they fill it, four key tiles a split at least
     const int64_t ctas = cdiv(Nq, 2 * kAttnQTile) * B * Hq, slots = kNumSM * (D == 128 ? 1 : 2);
-    const int64_t tiles = cdiv(Nk, attn_fwd_key_tile(static_cast<int>(D)));
+    const int64_t tiles = cdiv(Nk, D == 128 ? 128 : 64);
     pl.splits = ctas * 2 > slots ? 1 : static_cast<int>(std::max<int64_t>(1, std::min(slots / ctas, tiles / 4)));
   }
   size_t off = 256;   // error word
@@ -88,9 +88,14 @@ bool map_rows(CUtensorMap* m, const void* base, const long (&st)[3], int64_t B, 
   const CUtensorMapSwizzle sw = panel == 16   ? CU_TENSOR_MAP_SWIZZLE_32B
                                 : panel == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
                                               : CU_TENSOR_MAP_SWIZZLE_128B;
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  auto encode = [&] {
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  // a thread that has made no CUDA call yet (a backward's) has no context
+  // current, which a runtime call mends
+  return encode() || (cudaFree(nullptr) == cudaSuccess && encode());
 }
 
 // Rows that TMA reads: no broadcast (zero stride).
@@ -176,14 +181,13 @@ flare_status flare_attention_fwd(const flare_attention_args* a, void* workspace,
   p.part_o = reinterpret_cast<float*>(w + pl.off_part_o);
   p.part_l = reinterpret_cast<float*>(w + pl.off_part_l);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, kErrClearBytes, s) != cudaSuccess || !documents(a, pl, workspace, s))
-    return FLARE_ERR_LAUNCH;
+  if (!documents(a, pl, workspace, s)) return FLARE_ERR_LAUNCH;
   if (pl.step) {
     const AttnSide q{a->Q, r.q[0], r.q[1], r.q[2]}, k{a->K, r.k[0], r.k[1], r.k[2]}, v{a->V, r.v[0], r.v[1], r.v[2]};
     if (launch_attn_step(p, q, k, v, s) != cudaSuccess) return FLARE_ERR_LAUNCH;
   } else {
     AttnMaps m;
-    const int kt = attn_fwd_key_tile(p.D);
+    const int kt = attn_fwd_key_tile(p.D, p.slopes != nullptr, p.cap > 0.f);
     if (!map_rows(&m.q, a->Q, r.q, a->B, a->Hq, a->Nq, a->D, kAttnQTile) ||
         !map_rows(&m.k, a->K, r.k, a->B, a->Hk, a->Nk, a->D, kt) || !map_rows(&m.v, a->V, r.v, a->B, a->Hk, a->Nk, a->D, kt))
       return FLARE_ERR_LAUNCH;
@@ -216,8 +220,6 @@ flare_status flare_attention_bwd(const flare_attention_args* a, void* workspace,
   p.rows = reinterpret_cast<AttnRow*>(static_cast<uint8_t*>(workspace) + pl.off_rows);
   p.rows_pad = pl.rows_pad;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // launched first: a runtime call makes the device's context current, which
-  // a thread that has made none yet (a backward's) needs for the tensor maps
   if (!documents(a, pl, workspace, s) || launch_attn_rows(p, s) != cudaSuccess) return FLARE_ERR_LAUNCH;
   // the dQ pass keeps tiles of 128 rows of Q and dY and streams K and V; the dK/dV pass the other way round
   const int t = attn_bwd_stream_tile(p.a.D);

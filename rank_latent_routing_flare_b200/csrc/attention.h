@@ -65,7 +65,7 @@ struct AttnMaps {                // tensor maps of the kernels' operands
 // Runs of equal ids -> the document table of AttnMask.
 cudaError_t launch_attn_documents(const int32_t* ids, int2* doc, int B, int N, cudaStream_t s);
 
-int attn_fwd_key_tile(int D);    // keys per tile; the query tile is kAttnQTile rows
+int attn_fwd_key_tile(int D, bool bias, bool cap);   // keys per tile; the query tile is kAttnQTile rows
 constexpr int kAttnQTile = 128;
 cudaError_t launch_attn_fwd(const AttnMaps& m, const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t s);

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
   volatile int* range = reinterpret_cast<volatile int*>(sm + Cfg::OFF_MISC + 8);       // [2]
   volatile int* last_load = reinterpret_cast<volatile int*>(sm + Cfg::OFF_MISC + 32);  // [NST]
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // the dQ pass owns query heads and begins with the last rows, the dK/dV
   // pass owns key heads and begins with the first keys: under a causal mask
   // those have the most to do
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0 && N > 0) {
+    if (N > 0) {   // the whole warp, converged
       const uint32_t idesc_s = idesc_bf16_f32(128, T, false, false);
       const uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
       const uint64_t x1 = Tile::desc_k(sx), x2 = Tile::desc_k(sx + Cfg::X_B);
@@ -171,40 +171,48 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
       constexpr uint64_t TILE = Cfg::Y_B >> 4;
       auto issue_scores = [&](int n) -> bool {
         const int st = n % NST;
-        if (!mbar_wait_mma(y_full + st, (n / NST) & 1, wc)) return false;
+        if (!mbar_wait_warp(y_full + st, (n / NST) & 1, wc)) return false;
         tc_fence_after();
         const uint32_t col = tmem + Cfg::COL_S + (n & 1) * 2 * T;
         const uint64_t y1 = y_k + 2 * st * TILE, y2 = y1 + TILE;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss(col, x1 + Tile::kstep_k(kk, 128), y1 + Tile::kstep_k(kk, T), idesc_s, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_ss(col, x1 + Tile::kstep_k(kk, 128), y1 + Tile::kstep_k(kk, T), idesc_s, kk > 0 ? 1u : 0u);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss(col + T, x2 + Tile::kstep_k(kk, 128), y2 + Tile::kstep_k(kk, T), idesc_s, kk > 0 ? 1u : 0u);
-        umma_commit(s_full + (n & 1));
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_ss(col + T, x2 + Tile::kstep_k(kk, 128), y2 + Tile::kstep_k(kk, T), idesc_s, kk > 0 ? 1u : 0u);
+          umma_commit(s_full + (n & 1));
+        }
+        __syncwarp();
         return true;
       };
-      bool ok = mbar_wait_mma(x_full, 0, wc) && issue_scores(0);
+      bool ok = mbar_wait_warp(x_full, 0, wc) && issue_scores(0);
       if (ok && N > 1) ok = issue_scores(1);
       for (int n = 0; ok && n < N; ++n) {
         const int st = n % NST;
-        if (!mbar_wait_mma(p_full + (n & 1), (n >> 1) & 1, wc)) { ok = false; break; }
+        if (!mbar_wait_warp(p_full + (n & 1), (n >> 1) & 1, wc)) break;
         tc_fence_after();
         const uint32_t col = tmem + Cfg::COL_S + (n & 1) * 2 * T;
         const uint64_t y1 = y_mn + 2 * st * TILE, y2 = y1 + TILE;
-#pragma unroll
-        for (int ks = 0; ks < T / 16; ++ks)
-          umma_ts(tmem + Cfg::COL_OUT1, col + T + ks * 8, y1 + ks * Tile::KSTEP_MN, idesc_o, (n > 0 || ks > 0) ? 1u : 0u);
-        if (KV) {
+        if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < T / 16; ++ks)
-            umma_ts(tmem + Cfg::COL_OUT2, col + ks * 8, y2 + ks * Tile::KSTEP_MN, idesc_o, (n > 0 || ks > 0) ? 1u : 0u);
+            umma_ts(tmem + Cfg::COL_OUT1, col + T + ks * 8, y1 + ks * Tile::KSTEP_MN, idesc_o, (n > 0 || ks > 0) ? 1u : 0u);
+          if (KV) {
+#pragma unroll
+            for (int ks = 0; ks < T / 16; ++ks)
+              umma_ts(tmem + Cfg::COL_OUT2, col + ks * 8, y2 + ks * Tile::KSTEP_MN, idesc_o, (n > 0 || ks > 0) ? 1u : 0u);
+          }
+          umma_commit(y_empty + st);
         }
-        umma_commit(y_empty + st);
+        __syncwarp();
         if (n + 2 < N) ok = issue_scores(n + 2);
       }
-      umma_commit(all_done);
+      if (elect_one()) umma_commit(all_done);
+      __syncwarp();
       mbar_wait_drain(all_done, 0, p.timeout_ns);
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -213,8 +221,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
     const int row = x0 + tid;                       // query (dQ pass) or key of this lane
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     const uint32_t col_s = lane_base + Cfg::COL_S + w * 2 * T, col_g = col_s + T;
-    const float c2 = p.scale * kLog2e;
-    const float tanh_in = MOD && p.cap > 0.f ? 2.f * c2 / p.cap : 0.f, tanh_out = p.cap * kLog2e;
+    const ScoreOps ops(p.scale, p.cap, false);
     // dQ pass: this row's statistics
     AttnRow mine{INFINITY, 0.f, 0, 0};
     float slope2 = 0.f;
@@ -268,10 +275,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
               l2 = rs[y].l2;
               delta = rs[y].delta;
             }
-            float x = __uint_as_float(s[k + u]) * c2, dx = 1.f;
+            float x = __uint_as_float(s[k + u]) * ops.c2, dx = 1.f;
             if (MOD && p.cap > 0.f) {
-              const float t = tanh_exp(__uint_as_float(s[k + u]) * tanh_in);
-              x = t * tanh_out;
+              x = ops.capped(__uint_as_float(s[k + u]));
+              const float t = x / ops.out;
               dx = fmaf(-t, t, 1.f);
             }
             if (MOD && p.slopes) {

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "attention.h"
+#include "attn_math.cuh"
 #include "ptx.cuh"
 
 namespace flare {
@@ -58,12 +59,24 @@ __device__ __forceinline__ float bias_shift(const BatchMask& m, int i, int2 iv) 
   return static_cast<float>(d < 0 ? -d : d);
 }
 
-// tanh from 2^x and a reciprocal: 1 - 2 / (1 + e^(2u)); its error against
-// tanh is about 1e-7 absolute, of a result that the cap multiplies.
-__device__ __forceinline__ float tanh_exp(float u2log2e) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_mufu(u2log2e)));
-  return fmaf(-2.f, r, 1.f);
+// One lane of a converged warp, the same at every call.  The MMA warps run
+// their loops converged, with warp-uniform descriptors, and only issue under
+// this: an MMA issued from a branch on the lane number took about 80 clocks,
+// its operands having to be made uniform one by one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(ok));
+  return ok != 0;
+}
+
+// Registers of the executing warpgroup (all of its warps).
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // After tcgen05.wait::ld: the registers a TMEM load wrote are defined here,

@@ -27,20 +27,26 @@
 // no query may see (padding) are zeroed in shared memory by the softmax
 // threads before the product.
 //
-// D = 128: KT = 128, 512 TMEM columns, one CTA per SM.  D <= 64: the
-// exponentials bound the kernel; KT = 64 and 256 columns let two CTAs (four
-// softmax warps per SM sub-partition) share an SM.
+// D = 128, and capped or biased scores: KT = 128, 512 TMEM columns, one CTA per
+// SM whose softmax threads take over most of its registers.  Plain scores of D
+// <= 64: KT = 64 and 256 columns let two CTAs share an SM.  Measured on 2 x 16
+// heads x 4096^2, D = 64: plain 231 us (one CTA: 254), capped 303 (two CTAs,
+// which spill: 364), biased 303 (337); D = 128: plain 291, capped 325.
+#include <climits>
+
 #include "attn_common.cuh"
 
 namespace flare {
 namespace {
 
-template <int D>
+// MOD: 0 plain scores, 1 capped, 2 with a distance bias (and capped if p.cap > 0).
+template <int D, int MOD>
 struct FwdCfg {
   using Tile = RowTile<D>;
-  static constexpr int KT = D == 128 ? 128 : 64;
+  static constexpr bool WIDE = D == 128 || MOD != 0;
+  static constexpr int KT = WIDE ? 128 : 64;
   static constexpr int QT = kAttnQTile;
-  static constexpr int CTAS = D == 128 ? 1 : 2;
+  static constexpr int CTAS = WIDE ? 1 : 2;
   static constexpr int NST = D == 128 ? 2 : D == 64 ? 4 : 6;
   static constexpr int Q_B = Tile::bytes(QT), KV_B = Tile::bytes(KT);
   static constexpr int OFF_Q = 0;
@@ -52,7 +58,12 @@ struct FwdCfg {
   static constexpr int BYTES = OFF_MISC + 32 + 4 * NST;
   static constexpr uint32_t COL_S = 0, COL_O = 2 * KT;
   static constexpr uint32_t TMEM_COLS = COL_O + 2 * D <= 256 ? 256 : 512;
-  static constexpr int THREADS = 320;   // warps 0-3, 4-7: softmax; 8: loads; 9: MMAs
+  // Warps 0-3, 4-7: softmax; 8: loads; 9: MMAs.  One CTA an SM: two more fill
+  // a third warpgroup, which gives the softmax threads its registers (168 a
+  // thread at launch).
+  static constexpr int THREADS = WIDE ? 384 : 320;
+  static constexpr int LESS = 56, MORE = 224;
+  static_assert(256 * MORE + 128 * LESS <= 384 * 168, "register split");
   static_assert(COL_O + 2 * D <= TMEM_COLS && TMEM_COLS * CTAS <= 512, "TMEM columns");
   static_assert(KV_B % 1024 == 0 && Q_B % 1024 == 0, "tiles hold whole swizzle atoms");
 };
@@ -65,11 +76,107 @@ __device__ __forceinline__ int2 tile_range(const BatchMask& m, int r0, int KT) {
   return lo < hi ? make_int2(lo / KT, (hi + KT - 1) / KT) : make_int2(0, 0);
 }
 
-template <int D, bool MOD>
-__global__ void __launch_bounds__(FwdCfg<D>::THREADS, FwdCfg<D>::CTAS)
+__device__ __forceinline__ void unpair(uint64_t v, uint32_t& a, uint32_t& b) {
+  float x, y;
+  f2_unpack(v, x, y);
+  a = __float_as_uint(x);
+  b = __float_as_uint(y);
+}
+// -inf outside columns [first, last).
+template <int N>
+__device__ __forceinline__ void hide(uint32_t (&s)[N], int first, int last) {
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (k < first || k >= last) s[k] = 0xFF800000u;
+}
+// Raw products to capped scores in log2 units, + c.
+template <int N>
+__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], const ScoreOps& ops, bool small, float c) {
+  if (small) {
+    const uint64_t c2 = f2_dup(c);
+#pragma unroll
+    for (int k = 0; k < N; k += 2) unpair(ops.poly(f2(s[k], s[k + 1]), c2), s[k], s[k + 1]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] = __float_as_uint(fmaf(ops.tanh_any(as_f(s[k])), ops.out, c));
+  }
+}
+// s c2 minus slope2 |d - k| for column k.  Where every row of the warp stands
+// behind (side 1) or before (-1) all keys of the tile the bias is linear in k:
+// anchored every 16 columns and stepped in between, two columns an instruction.
+template <int N>
+__device__ __forceinline__ void bias_scores(uint32_t (&s)[N], float c2, float d, float slope2, int side) {
+  const uint64_t c = f2_dup(c2);
+  if (side != 0) {
+    const float g = side > 0 ? -slope2 : slope2;
+    const uint64_t step = f2_dup(-2.f * g);
+#pragma unroll
+    for (int k = 0; k < N; k += 16) {
+      uint64_t b = f2_pack(g * (d - k), g * (d - (k + 1)));
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        unpair(f2_fma(f2(s[k + i], s[k + i + 1]), c, b), s[k + i], s[k + i + 1]);
+        b = f2_add(b, step);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] = __float_as_uint(fmaf(as_f(s[k]), c2, -slope2 * fabsf(d - k)));
+  }
+}
+// Weights 2^(x - base) of a row's N columns, x = s c2 (RAW) or s, stored as
+// bf16 pairs from TMEM column `col` on; returns their sum.
+template <int N, bool RAW>
+__device__ __forceinline__ float weights(const uint32_t (&s)[N], float c2, float base, uint32_t col) {
+  const uint64_t c = f2_dup(c2), nb = f2_dup(-base);
+  uint64_t sum0 = f2_dup(0.f), sum1 = sum0;
+#pragma unroll
+  for (int k = 0; k < N; k += 32) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const uint64_t x = f2(s[k + 2 * q], s[k + 2 * q + 1]);
+      float p0, p1;
+      ex2_pair(RAW ? f2_fma(x, c, nb) : f2_add(x, nb), p0, p1);
+      if (q & 1) sum1 = f2_add(sum1, f2_pack(p0, p1));
+      else sum0 = f2_add(sum0, f2_pack(p0, p1));
+      pk[q] = pack_bf16x2(p0, p1);
+    }
+    tmem_st16(col + k / 2, pk);
+  }
+  float a, b;
+  f2_unpack(f2_add(sum0, sum1), a, b);
+  return a + b;
+}
+// As weights<N, true>, for capped scores of raw products: tanh and the shift
+// by the base in one polynomial.  Needs small.
+template <int N>
+__device__ __forceinline__ float capped_weights(const uint32_t (&s)[N], const ScoreOps& ops, float base, uint32_t col) {
+  const uint64_t nb = f2_dup(-base);
+  uint64_t sum0 = f2_dup(0.f), sum1 = sum0;
+#pragma unroll
+  for (int k = 0; k < N; k += 32) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      float p0, p1;
+      ex2_pair(ops.poly(f2(s[k + 2 * q], s[k + 2 * q + 1]), nb), p0, p1);
+      if (q & 1) sum1 = f2_add(sum1, f2_pack(p0, p1));
+      else sum0 = f2_add(sum0, f2_pack(p0, p1));
+      pk[q] = pack_bf16x2(p0, p1);
+    }
+    tmem_st16(col + k / 2, pk);
+  }
+  float a, b;
+  f2_unpack(f2_add(sum0, sum1), a, b);
+  return a + b;
+}
+
+template <int D, int MOD>
+__global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
-  using Cfg = FwdCfg<D>;
+  using Cfg = FwdCfg<D, MOD>;
   using Tile = RowTile<D>;
   constexpr int KT = Cfg::KT, QT = Cfg::QT, NST = Cfg::NST;
   extern __shared__ uint8_t smem_raw[];
@@ -89,14 +196,17 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, FwdCfg<D>::CTAS)
   volatile int* range = reinterpret_cast<volatile int*>(sm + Cfg::OFF_MISC + 8);       // [4]
   volatile int* last_load = reinterpret_cast<volatile int*>(sm + Cfg::OFF_MISC + 32);  // [NST]
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int BH = p.B * p.Hq, n_qt = gridDim.x / BH;
   // the last query tiles see the most keys under a causal mask: first
   const int qt = n_qt - 1 - static_cast<int>(blockIdx.x) / BH, bh = static_cast<int>(blockIdx.x) % BH;
   const int b = bh / p.Hq, h = bh % p.Hq, hk = h / p.G;
   const int q0 = qt * 2 * QT, split = blockIdx.y;
   const BatchMask mask = batch_mask(p.mask, b);
+  pdl_launch_dependents();   // the join of the splits
 
+  // The error word is clear before any wait can expire (seconds from now).
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 4) p.err[threadIdx.x] = 0u;
   if (threadIdx.x < 2) {
     const int2 r = tile_range(mask, q0 + threadIdx.x * QT, KT);
     range[2 * threadIdx.x] = r.x;
@@ -138,6 +248,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, FwdCfg<D>::CTAS)
     const int per = (jhi - jlo + p.splits - 1) / p.splits;
     jlo = min(jhi, jlo + split * per);
     jhi = min(jhi, jlo + per);
+#pragma unroll
     for (int w = 0; w < 2; ++w) {
       a[w] = max(a[w], jlo);
       e[w] = min(e[w], jhi);
@@ -146,69 +257,85 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, FwdCfg<D>::CTAS)
   }
   const int ntiles = jhi - jlo;
 
-  if (warp == 8) {
-    // ------------------------------------------------------------ loads
-    if (lane == 0 && ntiles > 0) {
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-      for (int w = 0; w < 2; ++w) {
-        mbar_arrive_expect_tx(q_full + w, Cfg::Q_B);   // rows behind the tensor's last come as zeros
-        Tile::load(sq + w * Cfg::Q_B, &tm_q, q_full + w, q0 + w * QT, h, b, QT);
-      }
-      for (int n = 0; n < ntiles; ++n) {
-        const int st = n % NST;
-        if (n >= NST && !mbar_wait(kv_empty + st, (n / NST - 1) & 1, wc)) break;
-        mbar_arrive_expect_tx(kv_full + st, 2 * Cfg::KV_B);
-        Tile::load(sk + st * Cfg::KV_B, &tm_k, kv_full + st, (jlo + n) * KT, hk, b, KT);
-        Tile::load(sv + st * Cfg::KV_B, &tm_v, kv_full + st, (jlo + n) * KT, hk, b, KT);
-        last_load[st] = n;
-      }
-    }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ MMAs
-    if (lane == 0 && ntiles > 0) {
-      const uint32_t idesc_s = idesc_bf16_f32(128, KT, false, false);
-      const uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
-      const uint64_t k_desc = Tile::desc_k(sk), v_desc = Tile::desc_mn(sv, KT);
-      auto issue_s = [&](int w, int n) -> bool {   // scores of tile n
-        const int st = n % NST;
-        if (!mbar_wait_mma(kv_full + st, (n / NST) & 1, wc)) return false;
-        tc_fence_after();
-        const uint64_t qd = Tile::desc_k(sq + w * Cfg::Q_B);
-        const uint64_t kd = k_desc + static_cast<uint64_t>((st * Cfg::KV_B) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss(tmem + Cfg::COL_S + w * KT, qd + Tile::kstep_k(kk, QT), kd + Tile::kstep_k(kk, KT), idesc_s,
-                  kk > 0 ? 1u : 0u);
-        umma_commit(s_full + w);
-        return true;
-      };
-      bool ok = mbar_wait_mma(q_full, 0, wc) && mbar_wait_mma(q_full + 1, 0, wc);
-      int used[2] = {0, 0};
-      for (int w = 0; ok && w < 2; ++w)
-        if (a[w] < e[w] && a[w] == jlo) ok = issue_s(w, 0);
-      for (int n = 0; ok && n < ntiles; ++n) {
-        const int j = jlo + n, st = n % NST;
-        for (int w = 0; ok && w < 2; ++w) {
-          if (j >= a[w] && j < e[w]) {
-            if (!mbar_wait_mma(p_full + w, used[w]++ & 1, wc)) { ok = false; break; }
-            tc_fence_after();
-            const uint64_t vd = v_desc + static_cast<uint64_t>((st * Cfg::KV_B) >> 4);
-#pragma unroll
-            for (int ks = 0; ks < KT / 16; ++ks)
-              umma_ts(tmem + Cfg::COL_O + w * D, tmem + Cfg::COL_S + w * KT + ks * 8, vd + ks * Tile::KSTEP_MN, idesc_o,
-                      (j > a[w] || ks > 0) ? 1u : 0u);
-            if (j + 1 == e[w]) umma_commit(o_full + w);
-          }
-          if (j + 1 >= a[w] && j + 1 < e[w]) ok = issue_s(w, n + 1);
+  if (warp >= 8) {
+    if constexpr (Cfg::WIDE) setmaxnreg_dec<Cfg::LESS>();
+    if (warp == 8) {
+      // ------------------------------------------------------------ loads
+      if (lane == 0 && ntiles > 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+        for (int w = 0; w < 2; ++w) {
+          mbar_arrive_expect_tx(q_full + w, Cfg::Q_B);   // rows behind the tensor's last come as zeros
+          Tile::load(sq + w * Cfg::Q_B, &tm_q, q_full + w, q0 + w * QT, h, b, QT);
         }
-        umma_commit(kv_empty + st);
+        for (int n = 0; n < ntiles; ++n) {
+          const int st = n % NST;
+          if (n >= NST && !mbar_wait(kv_empty + st, (n / NST - 1) & 1, wc)) break;
+          mbar_arrive_expect_tx(kv_full + st, 2 * Cfg::KV_B);
+          Tile::load(sk + st * Cfg::KV_B, &tm_k, kv_full + st, (jlo + n) * KT, hk, b, KT);
+          Tile::load(sv + st * Cfg::KV_B, &tm_v, kv_full + st, (jlo + n) * KT, hk, b, KT);
+          last_load[st] = n;
+        }
       }
-      umma_commit(all_done);   // every MMA issued above is done
-      mbar_wait_drain(all_done, 0, p.timeout_ns);
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ MMAs
+      if (ntiles > 0) {   // the whole warp, converged
+        const uint32_t idesc_s = idesc_bf16_f32(128, KT, false, false);
+        const uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
+        const uint64_t q_desc = Tile::desc_k(sq), k_desc = Tile::desc_k(sk), v_desc = Tile::desc_mn(sv, KT);
+        // scores of tile n, once it has landed
+        auto issue_s = [&](int w, int n) -> bool {
+          const int st = n % NST;
+          if (!mbar_wait_warp(kv_full + st, (n / NST) & 1, wc)) return false;
+          tc_fence_after();
+          const uint64_t qd = q_desc + static_cast<uint64_t>((w * Cfg::Q_B) >> 4);
+          const uint64_t kd = k_desc + static_cast<uint64_t>((st * Cfg::KV_B) >> 4);
+          if (elect_one()) {
+  #pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_ss(tmem + Cfg::COL_S + w * KT, qd + Tile::kstep_k(kk, QT), kd + Tile::kstep_k(kk, KT), idesc_s,
+                      kk > 0 ? 1u : 0u);
+            umma_commit(s_full + w);
+          }
+          __syncwarp();
+          return true;
+        };
+        bool ok = mbar_wait_warp(q_full, 0, wc) && mbar_wait_warp(q_full + 1, 0, wc);
+        int used[2] = {0, 0};
+  #pragma unroll
+        for (int w = 0; w < 2; ++w)
+          if (ok && a[w] < e[w] && a[w] == jlo) ok = issue_s(w, 0);
+        for (int n = 0; ok && n < ntiles; ++n) {
+          const int j = jlo + n, st = n % NST;
+  #pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (ok && j >= a[w] && j < e[w]) {
+              ok = mbar_wait_warp(p_full + w, used[w]++ & 1, wc);
+              tc_fence_after();
+              const uint64_t vd = v_desc + static_cast<uint64_t>((st * Cfg::KV_B) >> 4);
+              if (ok && elect_one()) {
+  #pragma unroll
+                for (int ks = 0; ks < KT / 16; ++ks)
+                  umma_ts(tmem + Cfg::COL_O + w * D, tmem + Cfg::COL_S + w * KT + ks * 8, vd + ks * Tile::KSTEP_MN,
+                          idesc_o, (j > a[w] || ks > 0) ? 1u : 0u);
+                if (j + 1 == e[w]) umma_commit(o_full + w);
+              }
+              __syncwarp();
+            }
+            if (ok && j + 1 >= a[w] && j + 1 < e[w]) ok = issue_s(w, n + 1);
+          }
+          if (elect_one()) umma_commit(kv_empty + st);
+          __syncwarp();
+        }
+        if (elect_one()) umma_commit(all_done);   // every MMA issued above is done
+        __syncwarp();
+        mbar_wait_drain(all_done, 0, p.timeout_ns);
+        __syncwarp();
+      }
     }
   } else {
+    if constexpr (Cfg::WIDE) setmaxnreg_inc<Cfg::MORE>();
     // ------------------------------------------------------------ softmax
     const int w = warp >> 2, wq = warp & 3;
     const int tid = threadIdx.x & 127;              // row of the tile; also the key whose V row it may zero
@@ -216,15 +343,15 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, FwdCfg<D>::CTAS)
     const int2 iv = row < p.mask.Nq ? row_interval(mask, row) : make_int2(0, 0);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     const uint32_t col_s = lane_base + Cfg::COL_S + w * KT, col_o = lane_base + Cfg::COL_O + w * D;
-    const float c2 = p.scale * kLog2e;
-    const float tanh_in = MOD && p.cap > 0.f ? 2.f * c2 / p.cap : 0.f, tanh_out = p.cap * kLog2e;
-    const float slope2 = MOD && p.slopes ? p.slopes[h] * kLog2e : 0.f;
+    const ScoreOps ops(p.scale, p.cap, true);
+    const bool capped = MOD == 1 || (MOD == 2 && p.cap > 0.f);
+    const float slope2 = MOD == 2 ? p.slopes[h] * kLog2e : 0.f;
     const int pos = bias_position(mask, row, iv);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    const int n_w = e[w] - a[w];
+    const int a_w = w ? a[1] : a[0], n_w = (w ? e[1] : e[0]) - a_w;
     for (int it = 0; it < n_w; ++it) {
-      const int j = a[w] + it, k0 = j * KT, n = j - jlo, st = n % NST;
+      const int j = a_w + it, k0 = j * KT, n = j - jlo, st = n % NST;
       // the V row this thread answers for: a key that no query may see
       bool dead = false;
       if (KT == 128 || tid < KT) {
@@ -241,64 +368,54 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, FwdCfg<D>::CTAS)
       tmem_ld_cols<KT>(col_s, s);
       tmem_wait_ld();
       regs_loaded(s);
-      if (MOD) {
-        if (p.cap > 0.f) {
-#pragma unroll
-          for (int k = 0; k < KT; ++k) s[k] = __float_as_uint(tanh_exp(__uint_as_float(s[k]) * tanh_in) * tanh_out);
+      const bool masked = !__all_sync(~0u, iv.x <= k0 && iv.y >= k0 + KT);   // some row does not see the whole tile
+      const int first = iv.x - k0, last = iv.y - k0;
+      // the row's maximum, in log2 units; scores that need more than a scale
+      // and a shift replace the products here
+      float mx;
+      bool small = false;
+      if (MOD == 0) {
+        if (masked) hide<KT>(s, first, last);
+        mx = max_of(s) * ops.c2;
+      } else if (MOD == 1) {
+        // tanh grows with its argument: the maximum takes it once
+        mx = max_of(s);
+        small = __all_sync(~0u, ops.small(fmaxf(mx, -min_of(s))));
+        if (masked || !small) {
+          cap_scores<KT>(s, ops, small, 0.f);
+          if (masked) hide<KT>(s, first, last);
+          mx = max_of(s);
         } else {
-#pragma unroll
-          for (int k = 0; k < KT; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * c2);
+          mx = ops.capped(mx);
         }
-        if (p.slopes) {
-          const int d0 = pos - k0;
-#pragma unroll
-          for (int k = 0; k < KT; ++k)
-            s[k] = __float_as_uint(fmaf(-slope2, fabsf(static_cast<float>(d0 - k)), __uint_as_float(s[k])));
-        }
+      } else {
+        if (capped) cap_scores<KT>(s, ops, __all_sync(~0u, ops.small(fmaxf(max_of(s), -min_of(s)))), 0.f);
+        const int side = __all_sync(~0u, pos >= k0 + KT - 1) ? 1 : __all_sync(~0u, pos <= k0) ? -1 : 0;
+        bias_scores<KT>(s, capped ? 1.f : ops.c2, static_cast<float>(pos - k0), slope2, side);
+        if (masked) hide<KT>(s, first, last);
+        mx = max_of(s);
       }
-      if (!__all_sync(~0u, iv.x <= k0 && iv.y >= k0 + KT)) {
-        const int first = iv.x - k0, last = iv.y - k0;
-#pragma unroll
-        for (int k = 0; k < KT; ++k)
-          if (k < first || k >= last) s[k] = 0xFF800000u;   // -inf
-      }
-      float mx = __uint_as_float(s[0]);
-#pragma unroll
-      for (int k = 1; k < KT; ++k) mx = fmaxf(mx, __uint_as_float(s[k]));
-      if (!MOD) mx *= c2;
       if (it == 0) {
         m = mx;
       } else if (__any_sync(~0u, mx > m + 8.f)) {
         const float m_new = fmaxf(m, mx);
-        const float f = m == -INFINITY ? 0.f : ex2_mufu(m - m_new);
+        const float fac = m == -INFINITY ? 0.f : ex2_mufu(m - m_new);
         m = m_new;
-        l *= f;
+        l *= fac;
 #pragma unroll
-        for (int d = 0; d < D; d += 16) {
+        for (int k = 0; k < D; k += 16) {
           uint32_t o[16];
-          tmem_ld16(col_o + d, o);
+          tmem_ld16(col_o + k, o);
           tmem_wait_ld();
           regs_loaded(o);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tmem_st16(col_o + d, o);
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(as_f(o[i]) * fac);
+          tmem_st16(col_o + k, o);
         }
       }
       const float base = m == -INFINITY ? 0.f : m;
-      float sum = 0.f;
-#pragma unroll
-      for (int c = 0; c < KT; c += 32) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float s0 = __uint_as_float(s[c + 2 * k]), s1 = __uint_as_float(s[c + 2 * k + 1]);
-          const float p0 = ex2_mufu(MOD ? s0 - base : fmaf(s0, c2, -base));
-          const float p1 = ex2_mufu(MOD ? s1 - base : fmaf(s1, c2, -base));
-          sum += p0 + p1;
-          pk[k] = pack_bf16x2(p0, p1);
-        }
-        tmem_st16(col_s + c / 2, pk);
-      }
+      const float sum = MOD == 1 && small && !masked ? capped_weights<KT>(s, ops, base, col_s)
+                                                     : weights<KT, MOD == 0>(s, ops.c2, base, col_s);
       l += sum;
       if (dead) {
         if (!mbar_wait(kv_full + st, (n / NST) & 1, wc)) ok = false;   // landed before the scores were computed
@@ -322,7 +439,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, FwdCfg<D>::CTAS)
       if (have) {
         if (p.splits > 1) p.part_l[part_row] = lse2;
         else if (p.L)
-          p.L[at] = lse2 * 0.69314718055994531f - (MOD && p.slopes && l > 0.f ? p.slopes[h] * bias_shift(mask, row, iv) : 0.f);
+          p.L[at] = lse2 * 0.69314718055994531f - (MOD == 2 && l > 0.f ? p.slopes[h] * bias_shift(mask, row, iv) : 0.f);
       }
       uint16_t* y = p.y + b * p.ys[0] + h * p.ys[1] + static_cast<long>(row) * p.ys[2];
 #pragma unroll
@@ -372,6 +489,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
   const long at = static_cast<long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (at >= rows) return;
   const int lane = threadIdx.x & 31;
+  pdl_wait();
   float top = -INFINITY;
   for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_l[s * rows + at]);
   const float base = top == -INFINITY ? 0.f : top;
@@ -403,130 +521,110 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
 }
 
 // Documents: the start and the end of the run of equal ids each position lies
-// in.  One CTA a batch entry; two passes of a running maximum (of the last
-// position where a run began) and a running minimum from the right.
-constexpr int kDocThreads = 1024, kDocPer = 8;
-template <bool MAX>
-__device__ __forceinline__ int block_scan(int v, int* sh) {   // inclusive, over the block, in thread order
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// in (the start twice where the id is negative).  A CTA takes 1024 positions:
+// a bit for each that begins a run, then the nearest bit on either side; the
+// ends of runs that reach into other chunks are searched for in the ids, 1024
+// at a time, so that no CTA waits on another.
+constexpr int kDocThreads = 256, kDocChunk = 1024;
+__global__ void __launch_bounds__(kDocThreads) attn_documents_kernel(const int32_t* ids, int2* doc, int N, int chunks) {
+  __shared__ uint32_t bits[kDocChunk / 32];
+  __shared__ int left, right;
+  const int b = blockIdx.x / chunks, c0 = (blockIdx.x - b * chunks) * kDocChunk;
+  ids += static_cast<long>(b) * N;
+  doc += static_cast<long>(b) * N;
+  auto begins = [&](int i) { return i <= 0 || i >= N || ids[i] != ids[i - 1]; };   // N begins what is behind
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = MAX ? __shfl_up_sync(~0u, v, o) : __shfl_down_sync(~0u, v, o);
-    if (MAX ? lane >= o : lane + o < 32) v = MAX ? max(v, u) : min(v, u);
+  for (int k = 0; k < kDocChunk; k += kDocThreads) {
+    const uint32_t w = __ballot_sync(~0u, begins(c0 + k + static_cast<int>(threadIdx.x)));
+    if ((threadIdx.x & 31) == 0) bits[(k + threadIdx.x) / 32] = w;
   }
-  if (lane == (MAX ? 31 : 0)) sh[warp] = v;
-  __syncthreads();
-  int t = sh[lane];
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = MAX ? __shfl_up_sync(~0u, t, o) : __shfl_down_sync(~0u, t, o);
-    if (MAX ? lane >= o : lane + o < 32) t = MAX ? max(t, u) : min(t, u);
+  if (threadIdx.x == 0) {
+    left = -1;
+    right = INT_MAX;
   }
-  const int other = __shfl_sync(~0u, t, MAX ? max(warp - 1, 0) : min(warp + 1, 31));
-  if (MAX ? warp > 0 : warp < 31) v = MAX ? max(v, other) : min(v, other);
   __syncthreads();
-  return v;
-}
-__global__ void __launch_bounds__(kDocThreads) attn_documents_kernel(const int32_t* ids, int2* doc, int N) {
-  __shared__ int sh[32];
-  __shared__ int carry;
-  ids += static_cast<long>(blockIdx.x) * N;
-  doc += static_cast<long>(blockIdx.x) * N;
-  constexpr int STEP = kDocThreads * kDocPer;
-  const int chunks = (N + STEP - 1) / STEP;
-  if (threadIdx.x == 0) carry = 0;
-  __syncthreads();
-  for (int c = 0; c < chunks; ++c) {
-    const int i0 = c * STEP + threadIdx.x * kDocPer;   // N < 2^30
-    int start[kDocPer], run = -1;
-#pragma unroll
-    for (int k = 0; k < kDocPer; ++k) {
-      const int i = i0 + k;
-      if (i < N && (i == 0 || ids[i] != ids[i - 1])) run = i;
-      start[k] = run;
-    }
-    const int before = block_scan<true>(run, sh);
-    int prev = __shfl_up_sync(~0u, before, 1);
-    if ((threadIdx.x & 31) == 31) sh[threadIdx.x >> 5] = before;
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) prev = threadIdx.x == 0 ? -1 : sh[(threadIdx.x >> 5) - 1];
-    prev = max(prev, carry);
-#pragma unroll
-    for (int k = 0; k < kDocPer; ++k)
-      if (i0 + k < N) doc[i0 + k].x = max(start[k], prev);
-    __syncthreads();
-    if (threadIdx.x == kDocThreads - 1) carry = max(carry, before);
+  // the run that reaches into the chunk from the left, and the one out of it
+  for (int lo = c0; (bits[0] & 1u) == 0 && left < 0;) {
+    lo -= kDocChunk;   // 0 begins a run, so this ends
+    int at = -1;
+    for (int i = lo + static_cast<int>(threadIdx.x); i < lo + kDocChunk; i += kDocThreads)
+      if (i >= 0 && begins(i)) at = i;
+    __syncthreads();   // the loop's test of `left` is done
+    if (at >= 0) atomicMax(&left, at);
     __syncthreads();
   }
-  if (threadIdx.x == 0) carry = N;
-  __syncthreads();
-  for (int c = chunks - 1; c >= 0; --c) {
-    const int i0 = c * STEP + threadIdx.x * kDocPer;
-    int end[kDocPer], run = N;
-#pragma unroll
-    for (int k = kDocPer - 1; k >= 0; --k) {
-      const int i = i0 + k;
-      if (i + 1 < N && ids[i + 1] != ids[i]) run = i + 1;
-      end[k] = run;
-    }
-    const int after = block_scan<false>(run, sh);
-    int next = __shfl_down_sync(~0u, after, 1);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = after;
+  for (int lo = c0 + kDocChunk; right == INT_MAX; lo += kDocChunk) {
+    int at = INT_MAX;
+    for (int i = lo + kDocChunk - kDocThreads + static_cast<int>(threadIdx.x); i >= lo; i -= kDocThreads)
+      if (begins(i)) at = min(i, N);
     __syncthreads();
-    if ((threadIdx.x & 31) == 31) next = threadIdx.x == kDocThreads - 1 ? N : sh[(threadIdx.x >> 5) + 1];
-    next = min(next, carry);
-#pragma unroll
-    for (int k = 0; k < kDocPer; ++k) {
-      const int i = i0 + k;
-      if (i < N) doc[i].y = ids[i] < 0 ? doc[i].x : min(end[k], next);
-    }
+    if (at != INT_MAX) atomicMin(&right, at);
     __syncthreads();
-    if (threadIdx.x == 0) carry = min(carry, after);
-    __syncthreads();
+  }
+  for (int k = threadIdx.x; k < kDocChunk; k += kDocThreads) {
+    const int i = c0 + k;
+    if (i >= N) break;
+    int w = k / 32;
+    uint32_t m = bits[w] & (~0u >> (31 - k % 32));          // bits up to k
+    while (m == 0 && w > 0) m = bits[--w];
+    const int start = m ? c0 + 32 * w + 31 - __clz(m) : left;
+    w = k / 32;
+    m = k % 32 == 31 ? 0u : bits[w] & (~0u << (k % 32 + 1));  // bits behind k
+    while (m == 0 && w < kDocChunk / 32 - 1) m = bits[++w];
+    const int end = m ? min(c0 + 32 * w + __ffs(m) - 1, N) : right;
+    doc[i] = make_int2(start, ids[i] < 0 ? start : end);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_attn_documents(const int32_t* ids, int2* doc, int B, int N, cudaStream_t s) {
-  attn_documents_kernel<<<B, kDocThreads, 0, s>>>(ids, doc, N);
+  const int chunks = (N + kDocChunk - 1) / kDocChunk;
+  attn_documents_kernel<<<static_cast<unsigned>(static_cast<long>(B) * chunks), kDocThreads, 0, s>>>(ids, doc, N, chunks);
   return cudaGetLastError();
 }
 
-int attn_fwd_key_tile(int D) { return D == 128 ? FwdCfg<128>::KT : FwdCfg<64>::KT; }
+namespace {
+// Calls f with the kernel's configuration for these scores.
+template <typename F>
+auto by_config(const int D, bool bias, bool cap, F&& f) {
+  auto by_mod = [&](auto d) {
+    constexpr int DD = decltype(d)::value;
+    return bias  ? f(d, std::integral_constant<int, 2>{}, FwdCfg<DD, 2>{})
+           : cap ? f(d, std::integral_constant<int, 1>{}, FwdCfg<DD, 1>{})
+                 : f(d, std::integral_constant<int, 0>{}, FwdCfg<DD, 0>{});
+  };
+  return D == 16   ? by_mod(std::integral_constant<int, 16>{})
+         : D == 32 ? by_mod(std::integral_constant<int, 32>{})
+         : D == 64 ? by_mod(std::integral_constant<int, 64>{})
+                   : by_mod(std::integral_constant<int, 128>{});
+}
+}  // namespace
+
+int attn_fwd_key_tile(int D, bool bias, bool cap) {
+  return by_config(D, bias, cap, [](auto, auto, auto c) { return decltype(c)::KT; });
+}
 
 cudaError_t launch_attn_fwd(const AttnMaps& m, const AttnParams& p, cudaStream_t s) {
   const int n_qt = (p.mask.Nq + 2 * kAttnQTile - 1) / (2 * kAttnQTile);
   const dim3 grid(static_cast<unsigned>(static_cast<long>(n_qt) * p.B * p.Hq), static_cast<unsigned>(p.splits));
-  auto go = [&](auto kern, int bytes, int threads, int ctas) {
-    // at most `ctas` CTAs share an SM, so that each finds its TMEM columns free
-    const int floor = 228 * 1024 / (ctas + 1) + 1024;
-    const int smem = bytes + 1024 > floor ? bytes + 1024 : floor;
+  return by_config(p.D, p.slopes != nullptr, p.cap > 0.f, [&](auto d, auto mod, auto c) {
+    using C = decltype(c);
+    auto* kern = attn_fwd_kernel<decltype(d)::value, decltype(mod)::value>;
+    // at most CTAS CTAs share an SM, so that each finds its TMEM columns free
+    constexpr int floor = 228 * 1024 / (C::CTAS + 1) + 1024;
+    constexpr int smem = C::BYTES + 1024 > floor ? C::BYTES + 1024 : floor;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, threads, smem, s>>>(m.q, m.k, m.v, p);
+    kern<<<grid, C::THREADS, smem, s>>>(m.q, m.k, m.v, p);
     return cudaGetLastError();
-  };
-  const bool mod = p.cap > 0.f || p.slopes;
-  auto by_mod = [&](auto d) {
-    constexpr int D = decltype(d)::value;
-    using C = FwdCfg<D>;
-    return mod ? go(attn_fwd_kernel<D, true>, C::BYTES, C::THREADS, C::CTAS)
-               : go(attn_fwd_kernel<D, false>, C::BYTES, C::THREADS, C::CTAS);
-  };
-  switch (p.D) {
-    case 16: return by_mod(std::integral_constant<int, 16>{});
-    case 32: return by_mod(std::integral_constant<int, 32>{});
-    case 64: return by_mod(std::integral_constant<int, 64>{});
-    case 128: return by_mod(std::integral_constant<int, 128>{});
-  }
-  return cudaErrorInvalidValue;
+  });
 }
 
 cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t s) {
   const long rows = static_cast<long>(p.B) * p.Hq * p.mask.Nq;
-  attn_join_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  LaunchCfg lc(dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, true);
+  return cudaLaunchKernelEx(&lc.cfg, attn_join_kernel, p);
 }
 
 }  // namespace flare

@@ -92,10 +92,12 @@ __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_k
   const int split = blockIdx.x % a.splits, bk = blockIdx.x / a.splits, b = bk / a.Hk, hk = bk % a.Hk;
   const int rows = a.G * a.mask.Nq;
   const BatchMask mask = batch_mask(a.mask, b);
+  pdl_launch_dependents();   // the join of the splits
 
   // the keys that any row sees, rounded to chunks and dealt to the splits
   int lo = 0, hi = 0;
   const int last_row = min(a.mask.Nq, mask.qlen) - 1;
+  if (blockIdx.x == 0 && threadIdx.x < 4) a.err[threadIdx.x] = 0u;   // nothing here can wait in vain
   if (last_row >= 0) {
     lo = row_interval(mask, 0).x / kChunk * kChunk;
     hi = row_interval(mask, last_row).y;
@@ -109,8 +111,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_k
   int pos[2];
   float slope2[2];
   uint32_t qf[D / 16][4];
-  const float c2 = a.scale * kLog2e;
-  const float tanh_in = a.cap > 0.f ? 2.f * c2 / a.cap : 0.f, tanh_out = a.cap * kLog2e;
+  const ScoreOps ops(a.scale, a.cap, true);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int r = g + 8 * u, i = r / a.G, h = hk * a.G + r % a.G;
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_k
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int u = k >> 1, key = key0 + 8 * n + 2 * t + (k & 1);
-        float x = a.cap > 0.f ? tanh_exp(s[n][k] * tanh_in) * tanh_out : s[n][k] * c2;
+        float x = a.cap > 0.f ? ops.capped(s[n][k]) : s[n][k] * ops.c2;
         if (a.slopes) x = fmaf(-slope2[u], fabsf(static_cast<float>(pos[u] - key)), x);
         if (key < iv[u].x || key >= iv[u].y) x = -INFINITY;
         s[n][k] = x;

@@ -9,86 +9,84 @@ include/flare_ops.h.
 """
 from __future__ import annotations
 
+import functools
 import struct
 
 import torch
 
-from . import _binding as b
-from ._rows import ROW_WIDTHS, call, check_rows, check_small, ptr, rows, same_device, workspace as _ws
+from ._rows import NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, entry, ptr, rows, workspace as _ws
 
 # flare_qk_norm_rope_args
 _ARGS = struct.Struct("=9qd3q4q4q2q2q4q4q4q4q2q")
+_f32, _i32 = torch.float32, torch.int32
 
 
+@functools.lru_cache(maxsize=4096)
 def flare_qk_norm_rope_workspace_bytes(B: int, N: int, Hq: int, Hk: int, D: int) -> int:
-    return int(b.load_library().flare_qk_norm_rope_workspace_bytes(B, N, Hq, Hk, D))
+    return int(entry("flare_qk_norm_rope_workspace_bytes")(B, N, Hq, Hk, D))
 
 
-def _sizes(Q, K, freqs, positions, lengths, q_gain, k_gain, check):
+def _head(Q, K, q_gain, k_gain, freqs, positions, lengths, eps, interleaved, check):
+    """The inputs' part of the argument struct, in its order, and (B, N, D, Hq, Hk, device index)."""
     X = Q if Q is not None else K
     if X is None:
         raise ValueError("Q and K are both None")
     if X.dim() != 4 or (K is not None and K.dim() != 4):
         raise ValueError("Q and K are [B, H, N, D]")
-    B, _, N, D = X.shape
-    Hq = 0 if Q is None else Q.shape[1]
+    B, H, N, D = X.shape
+    Hq = 0 if Q is None else H
     Hk = 0 if K is None else K.shape[1]
-    rot, axes, kind = 0, 0, 0
+    rot = axes = kind = 0
     if freqs is not None:
-        axes, rot = (1, 2 * freqs.shape[0]) if freqs.dim() == 1 else (freqs.shape[0], 2 * freqs.shape[-1])
-        kind = 0 if positions is None else 1 if positions.dtype == torch.int32 else 2
+        f = freqs.shape
+        axes, rot = (1, 2 * f[0]) if len(f) == 1 else (f[0], 2 * f[-1])
+        kind = 0 if positions is None else 1 if positions.dtype is _i32 else 2
+    dev = X.get_device()
     if check:
-        dev = X.device
+        if not X.is_cuda:
+            raise TypeError("Q and K must be CUDA tensors")
         if D not in ROW_WIDTHS:
             raise ValueError(f"D is {D}, expected one of {ROW_WIDTHS}")
-        for name, t, H in (("Q", Q, Hq), ("K", K, Hk)):
-            if t is not None:
-                check_rows(name, t, (B, H, N, D))
-        same_device(dev, Q=Q, K=K)
-        for name, g, H in (("q_gain", q_gain, Hq), ("k_gain", k_gain, Hk)):
+        q = NO_ROWS if Q is None else check_rows("Q", Q, (B, Hq, N, D), dev)
+        k = NO_ROWS if K is None else check_rows("K", K, (B, Hk, N, D), dev)
+        for name, g, h in (("q_gain", q_gain, Hq), ("k_gain", k_gain, Hk)):
             if g is not None:
-                if H == 0:
+                if h == 0:
                     raise ValueError(f"{name} is given without its tensor")
-                check_small(name, g, torch.float32, (D,) if g.dim() == 1 else (H, D), dev)
+                check_small(name, g, _f32, (D,) if g.dim() == 1 else (h, D), dev)
         if freqs is None:
             if positions is not None:
                 raise ValueError("positions are given without freqs")
         else:
-            if freqs.dim() not in (1, 2):
+            if len(f) not in (1, 2):
                 raise ValueError("freqs is [rot / 2] or [axes, rot / 2]")
-            check_small("freqs", freqs, torch.float32, None, dev)
+            check_small("freqs", freqs, _f32, None, dev)
             if kind == 1:
-                check_small("positions", positions, torch.int32, (B, N), dev)
+                check_small("positions", positions, _i32, (B, N), dev)
             elif kind == 2:
-                shapes = ((B, N, axes), (B, N)) if axes == 1 else ((B, N, axes),)
-                check_small("positions", positions, torch.float32,
-                            positions.shape if tuple(positions.shape) in shapes else shapes[0], dev)
+                check_small("positions", positions, _f32, (B, N) if axes == 1 and positions.dim() == 2 else (B, N, axes), dev)
             if kind != 2 and axes != 1:
                 raise ValueError("more than one axis of frequencies needs real coordinates (float32 positions)")
-        check_small("lengths", lengths, torch.int32, (B,), dev)
-    return B, N, D, Hq, Hk, rot, axes, kind, X.device
+        check_small("lengths", lengths, _i32, (B,), dev)
+    else:
+        q, k = (NO_ROWS if t is None else rows(t) for t in (Q, K))
+    packed = (B, N, D, Hq, Hk, rot, axes, bool(interleaved), kind, eps, ptr(freqs), ptr(positions), ptr(lengths), *q, *k,
+              ptr(q_gain), ptr(k_gain), q_gain is not None and q_gain.dim() == 2,
+              k_gain is not None and k_gain.dim() == 2)
+    return packed, (B, N, D, Hq, Hk, dev)
 
 
-def _pack(sizes, interleaved, eps, freqs, positions, lengths, Q, K, q_gain, k_gain, Qr, Kr, dQ=None, dK=None,
-          dq_gain=None, dk_gain=None):
-    B, N, D, Hq, Hk, rot, axes, kind, _ = sizes
-    return _ARGS.pack(B, N, D, Hq, Hk, rot, axes, bool(interleaved), kind, eps, ptr(freqs), ptr(positions),
-                      ptr(lengths), *rows(Q), *rows(K), ptr(q_gain), ptr(k_gain),
-                      q_gain is not None and q_gain.dim() == 2, k_gain is not None and k_gain.dim() == 2, *rows(Qr),
-                      *rows(Kr), *rows(dQ), *rows(dK), ptr(dq_gain), ptr(dk_gain))
-
-
-def _output(name, t, like, check):
+def _output(name, t, like, dev, check):
+    """An output of `like`'s shape, new unless given, and its pointer and strides."""
     if like is None:
         if t is not None:
             raise ValueError(f"{name} is given without its input")
-        return None
+        return None, NO_ROWS
     if t is None:
-        return torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
-    if check:
-        check_rows(name, t, tuple(like.shape), output=True)
-        same_device(like.device, **{name: t})
-    return t
+        t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    elif check:
+        return t, check_rows(name, t, like.shape, dev, output=True)
+    return t, rows(t)
 
 
 def flare_qk_norm_rope_fwd(Q=None, K=None, q_gain=None, k_gain=None, freqs=None, positions=None, lengths=None,
@@ -104,10 +102,11 @@ def flare_qk_norm_rope_fwd(Q=None, K=None, q_gain=None, k_gain=None, freqs=None,
     float32 [B, N, axes] coordinates.  Pairs are (p, p + rot/2), with rot a
     multiple of 16, or (2p, 2p + 1) when ``interleaved``.  Rows n >=
     lengths[b] (int32 [B]) are not read and come out as zeros."""
-    sizes = _sizes(Q, K, freqs, positions, lengths, q_gain, k_gain, check)
-    Qr, Kr = _output("Qr", Qr, Q, check), _output("Kr", Kr, K, check)
-    args = _pack(sizes, interleaved, eps, freqs, positions, lengths, Q, K, q_gain, k_gain, Qr, Kr)
-    call(b.load_library().flare_qk_norm_rope_fwd, "flare_qk_norm_rope_fwd", sizes[-1], stream, args)
+    head, (*_, dev) = _head(Q, K, q_gain, k_gain, freqs, positions, lengths, eps, interleaved, check)
+    Qr, q = _output("Qr", Qr, Q, dev, check)
+    Kr, k = _output("Kr", Kr, K, dev, check)
+    args = _ARGS.pack(*head, *q, *k, *NO_ROWS, *NO_ROWS, 0, 0)
+    call("flare_qk_norm_rope_fwd", "flare_qk_norm_rope_fwd", dev, stream, args)
     return Qr, Kr
 
 
@@ -118,30 +117,28 @@ def flare_qk_norm_rope_bwd(Q=None, K=None, dQr=None, dKr=None, q_gain=None, k_ga
     a dict: dQ, dK (bf16 [B,H,N,D]) and dq_gain, dk_gain (float32, the gains'
     shapes), None for what is absent.  ``grads`` may hold preallocated outputs
     by name; dQ and dK may be strided views (slices of a packed gradient)."""
-    sizes = _sizes(Q, K, freqs, positions, lengths, q_gain, k_gain, check)
-    B, N, D, Hq, Hk, _, _, _, dev = sizes
+    head, (B, N, D, Hq, Hk, dev) = _head(Q, K, q_gain, k_gain, freqs, positions, lengths, eps, interleaved, check)
+    dy = []
     for name, t, x in (("dQr", dQr, Q), ("dKr", dKr, K)):
         if (t is None) != (x is None):
             raise ValueError(f"{name} goes with its input")
-        if check and t is not None:
-            check_rows(name, t, tuple(x.shape))
-            same_device(dev, **{name: t})
+        dy += NO_ROWS if t is None else check_rows(name, t, x.shape, dev) if check else rows(t)
     g = dict(grads or {})
-    g["dQ"], g["dK"] = _output("dQ", g.get("dQ"), Q, check), _output("dK", g.get("dK"), K, check)
+    g["dQ"], q = _output("dQ", g.get("dQ"), Q, dev, check)
+    g["dK"], k = _output("dK", g.get("dK"), K, dev, check)
     for name, gain in (("dq_gain", q_gain), ("dk_gain", k_gain)):
         if gain is None:
             g[name] = None
         elif g.get(name) is None:
             g[name] = torch.empty_like(gain)
         elif check:
-            check_small(name, g[name], torch.float32, tuple(gain.shape), dev)
-    ws = None
+            check_small(name, g[name], _f32, gain.shape, dev)
+    ws, nbytes = 0, 0
     if q_gain is not None or k_gain is not None:
-        ws = _ws(workspace, flare_qk_norm_rope_workspace_bytes(B, N, Hq, Hk, D), dev)
-    args = _pack(sizes, interleaved, eps, freqs, positions, lengths, Q, K, q_gain, k_gain, dQr, dKr, g["dQ"], g["dK"],
-                 g["dq_gain"], g["dk_gain"])
-    call(b.load_library().flare_qk_norm_rope_bwd, "flare_qk_norm_rope_bwd", dev, stream, args, ptr(ws),
-         0 if ws is None else ws.numel())
+        workspace = _ws(workspace, flare_qk_norm_rope_workspace_bytes(B, N, Hq, Hk, D), Q if Q is not None else K)
+        ws, nbytes = workspace.data_ptr(), workspace.numel()
+    args = _ARGS.pack(*head, *dy, *q, *k, ptr(g["dq_gain"]), ptr(g["dk_gain"]))
+    call("flare_qk_norm_rope_bwd", "flare_qk_norm_rope_bwd", dev, stream, args, ws, nbytes)
     return g
 
 
