@@ -34,7 +34,7 @@ flare_status check_sizes(int64_t B, int64_t Hq, int64_t Hk, int64_t Nq, int64_t 
 struct AttnPlan {
   bool step;           // few rows: attn_step
   int splits;
-  int rows_pad;        // backward
+  int row_blocks;      // backward
   size_t off_doc, off_part_o, off_part_l, off_rows, total;
 };
 
@@ -60,9 +60,9 @@ AttnPlan make_attn_plan(int64_t B, int64_t Hq, int64_t Hk, int64_t Nq, int64_t N
   const size_t rows = static_cast<size_t>(B * Hq * Nq);
   if (backward) {
     const int64_t t = attn_bwd_stream_tile(static_cast<int>(D));
-    pl.rows_pad = static_cast<int>(cdiv(Nq, t) * t);
+    pl.row_blocks = static_cast<int>(cdiv(Nq, t));
     pl.off_rows = off;
-    off += align256(static_cast<size_t>(B * Hq) * pl.rows_pad * sizeof(AttnRow));
+    off += align256(static_cast<size_t>(B * Hq) * pl.row_blocks * t * kAttnRowFields * 4);
   } else if (pl.splits > 1) {
     pl.off_part_o = off;
     off += align256(rows * pl.splits * D * 4);
@@ -217,8 +217,8 @@ flare_status flare_attention_bwd(const flare_attention_args* a, void* workspace,
   p.dq = a->dQ;
   p.dk = a->dK;
   p.dv = a->dV;
-  p.rows = reinterpret_cast<AttnRow*>(static_cast<uint8_t*>(workspace) + pl.off_rows);
-  p.rows_pad = pl.rows_pad;
+  p.rows = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.off_rows);
+  p.row_blocks = pl.row_blocks;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!documents(a, pl, workspace, s) || launch_attn_rows(p, s) != cudaSuccess) return FLARE_ERR_LAUNCH;
   // the dQ pass keeps tiles of 128 rows of Q and dY and streams K and V; the dK/dV pass the other way round

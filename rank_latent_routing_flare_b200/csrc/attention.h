@@ -40,22 +40,20 @@ struct AttnParams {
   unsigned long long timeout_ns;
 };
 
-// One row's statistics for the backward, [B][Hq][Nq padded to kAttnRowPad]:
-// P = 2^(x - l2) (l2 = +inf: the row sees nothing), delta = <dY, Y>, the
-// interval of keys it sees.
-struct __align__(16) AttnRow {
-  float l2, delta;
-  int lo, hi;
-};
-constexpr int kAttnRowPad = 128;
+// Statistics of the backward's query rows: per batch entry and query head,
+// blocks of T = attn_bwd_stream_tile(D) rows, each kAttnRowFields arrays of T
+// 4-byte values: -l2 (P = 2^(x - l2); -inf: the row sees nothing), -delta
+// (delta = <dY, Y>), the interval [lo, hi) of keys that it sees, and its
+// position for the distance bias.
+constexpr int kAttnRowFields = 5;
 
 struct AttnBwdParams {
   AttnParams a;
   AttnSide dy, yin;
   uint16_t *dq, *dk, *dv;
   long dqs[3], dks[3], dvs[3];
-  AttnRow* rows;
-  int rows_pad;                  // rows per head: Nq rounded up to kAttnRowPad
+  float* rows;
+  int row_blocks;                // blocks per head
 };
 
 struct AttnMaps {                // tensor maps of the kernels' operands

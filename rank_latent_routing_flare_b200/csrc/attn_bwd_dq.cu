@@ -6,17 +6,17 @@ namespace flare {
 namespace {
 
 // One row's statistics: l2 = L log2(e), moved by the distance that the bias
-// positions leave out (+inf: the row sees nothing), delta = <dY, Y> in fp32,
-// and its interval of keys.  D / 8 lanes a row, 16-byte loads.
+// positions leave out, and delta = <dY, Y> in fp32.  D / 8 lanes a row, 16-byte
+// loads.
 template <int D>
 __global__ void __launch_bounds__(256) attn_rows_kernel(const AttnBwdParams bp) {
-  constexpr int L = D / 8, ROWS = 256 / L;
+  constexpr int L = D / 8, ROWS = 256 / L, T = BwdCfg<D>::T;
   const AttnParams& p = bp.a;
-  const long blocks = (bp.rows_pad + ROWS - 1) / ROWS;
+  const int rows = bp.row_blocks * T, blocks = (rows + ROWS - 1) / ROWS;
   const long bh = blockIdx.x / blocks;
-  const int i = static_cast<int>(blockIdx.x % blocks) * ROWS + threadIdx.x / L, l = threadIdx.x % L;
+  const int i = static_cast<int>(blockIdx.x - bh * blocks) * ROWS + threadIdx.x / L, l = threadIdx.x % L;
   const int b = static_cast<int>(bh / p.Hq), h = static_cast<int>(bh % p.Hq);
-  if (bh == 0 && blockIdx.x == 0 && threadIdx.x < 4) p.err[threadIdx.x] = 0u;
+  if (blockIdx.x == 0 && threadIdx.x < 4) p.err[threadIdx.x] = 0u;
   const BatchMask m = batch_mask(p.mask, b);
   const int2 iv = row_interval(m, i);
   const bool sees = i < p.mask.Nq && iv.x < iv.y;
@@ -30,17 +30,19 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const AttnBwdParams bp) 
   }
 #pragma unroll
   for (int o = L / 2; o > 0; o >>= 1) delta += __shfl_xor_sync(~0u, delta, o);
-  if (l == 0 && i < bp.rows_pad) {
-    AttnRow r{INFINITY, 0.f, iv.x, iv.y};
+  if (l == 0 && i < rows) {
+    float l2 = INFINITY;
     if (sees) {
       float L2 = p.L[bh * p.mask.Nq + i];
       if (p.slopes) L2 += p.slopes[h] * bias_shift(m, i, iv);
-      if (L2 != -INFINITY) {
-        r.l2 = L2 * kLog2e;
-        r.delta = delta;
-      }
+      if (L2 != -INFINITY) l2 = L2 * kLog2e;
     }
-    bp.rows[bh * bp.rows_pad + i] = r;
+    float* r = bp.rows + (bh * bp.row_blocks + i / T) * (kAttnRowFields * T) + i % T;
+    r[0] = -l2;
+    r[T] = l2 == INFINITY ? 0.f : -delta;
+    r[2 * T] = __int_as_float(iv.x);
+    r[3 * T] = __int_as_float(iv.y);
+    r[4 * T] = __int_as_float(bias_position(m, i, iv));
   }
 }
 
@@ -51,7 +53,7 @@ int attn_bwd_stream_tile(int D) { return D >= 64 ? BwdCfg<64>::T : BwdCfg<32>::T
 cudaError_t launch_attn_rows(const AttnBwdParams& p, cudaStream_t s) {
   auto go = [&](auto d) {
     constexpr int D = decltype(d)::value, ROWS = 256 / (D / 8);
-    const long blocks = (p.rows_pad + ROWS - 1) / ROWS;
+    const long blocks = (static_cast<long>(p.row_blocks) * BwdCfg<D>::T + ROWS - 1) / ROWS;
     attn_rows_kernel<D><<<static_cast<unsigned>(blocks * p.a.B * p.a.Hq), 256, 0, s>>>(p);
     return cudaGetLastError();
   };

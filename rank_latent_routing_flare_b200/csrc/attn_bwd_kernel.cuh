@@ -10,24 +10,34 @@
 // tiles of T rows of the other side:
 //
 //   dQ pass  rows: queries (Q, dY), stream: keys (K, V)
-//     S = Q K^T, G = dY V^T, out1 += dS K
+//     S = Q K^T, G = dY V^T, out1 += dS K, dS as two bf16 parts
 //   dK/dV pass  rows: keys (K, V), stream: the rows (Q, dY) of every query
 //     head of the key head, S = K Q^T, G = V dY^T, out1 += dS Q, out2 += P dY
 //
 // The rows are TMEM lanes (UMMA M = 128).  The two warpgroups take stream
 // tiles in turn: each has its own S and G columns and both add to the same
 // accumulators.  Weights and dS are written over S and G as bf16 and read from
-// there as the products' A operands; the MMA thread issues tile n's products
+// there as the products' A operands; the MMA warp issues tile n's products
 // and right behind them the scores of tile n + 2 into the same columns (the
 // tensor pipe runs in order), while the other warpgroup works on tile n + 1.
 // Row statistics (l2, delta, interval) are held in registers in the dQ pass
 // and come with the stream in the dK/dV pass.
 //
+// Roundings.  dS in bf16 is off by up to 2^-8 and would make dQ half again as
+// inexact as its own rounding to bf16; the dQ pass, whose S columns are free,
+// keeps dS - bf16(dS) there and adds its product too.  delta from the rounded
+// Y would do the same to dK where a row sees few keys: the dQ pass sums delta
+// = sum_j P_ij g_ij in fp32 on the way and leaves it for the dK/dV pass.  L in
+// fp32 is coarse where the scores are far from 0 (a row far from its keys under
+// a distance bias): the dQ pass also sums P, which should be 1, divides by it
+// and corrects l2 for the other pass.
+//
 // Streamed rows that take no part (padding) are zeroed in shared memory
 // before the products read them: a weight of 0 does not erase a NaN.
 //
-// D >= 64: T = 64, up to 512 TMEM columns, one CTA per SM.  D <= 32: T = 48,
-// 256 columns, two CTAs per SM; the exponentials bound those.
+// D >= 64: T = 64, up to 512 TMEM columns, one CTA per SM whose softmax threads
+// take over most of its registers.  D <= 32: T = 48, 256 columns, two CTAs per
+// SM; the exponentials bound those.
 #pragma once
 
 #include "attn_common.cuh"
@@ -42,7 +52,7 @@ struct BwdCfg {
   static constexpr int CH = D >= 64 ? 32 : 16;           // columns of a tile computed at once
   static constexpr int CTAS = D >= 64 ? 1 : 2;
   static constexpr int NST = D == 128 ? 4 : 6;
-  static constexpr int X_B = Tile::bytes(128), Y_B = Tile::bytes(T), R_B = 1024;
+  static constexpr int X_B = Tile::bytes(128), Y_B = Tile::bytes(T), R_B = kAttnRowFields * T * 4;
   static constexpr int OFF_X = 0;                         // X1 | X2
   static constexpr int OFF_Y = OFF_X + 2 * X_B;           // NST x (Y1 | Y2)
   static constexpr int OFF_R = OFF_Y + 2 * NST * Y_B;     // NST x row statistics (dK/dV pass)
@@ -51,12 +61,18 @@ struct BwdCfg {
   static constexpr int BYTES = OFF_MISC + 32 + 4 * NST;
   static constexpr uint32_t COL_S = 0, COL_OUT1 = 4 * T, COL_OUT2 = 4 * T + D;   // buffer g: S at 2 T g, G at 2 T g + T
   static constexpr uint32_t TMEM_COLS = COL_OUT2 + D <= 256 ? 256 : 512;
-  static constexpr int THREADS = 320;                     // warps 0-3, 4-7: softmax; 8: loads; 9: MMAs
+  // Warps 0-3, 4-7: softmax; 8: loads; 9: MMAs.  One CTA an SM: two more fill a
+  // third warpgroup, which gives the softmax threads its registers (168 a
+  // thread at launch).
+  static constexpr bool WIDE = CTAS == 1;
+  static constexpr int THREADS = WIDE ? 384 : 320, LESS = 56, MORE = 224;
+  static_assert(256 * MORE + 128 * LESS <= 384 * 168, "register split");
   static_assert(COL_OUT2 + D <= TMEM_COLS && TMEM_COLS * CTAS <= 512, "TMEM columns");
-  static_assert(Y_B % (8 * Tile::ROWB) == 0 && X_B % 1024 == 0 && T * 16 <= R_B, "tiles hold whole swizzle atoms");
+  static_assert(Y_B % (8 * Tile::ROWB) == 0 && X_B % 1024 == 0 && R_B % 64 == 0, "tiles hold whole swizzle atoms");
 };
 
-template <int D, bool KV, bool MOD>
+// MOD: 0 plain scores, 1 capped, 2 with a distance bias (and capped if p.cap > 0).
+template <int D, bool KV, int MOD>
 __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_x2,
                     const __grid_constant__ CUtensorMap tm_y1, const __grid_constant__ CUtensorMap tm_y2,
@@ -137,84 +153,90 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
   const int t_lo = range[0], per_head = max(0, range[1] - range[0]);
   const int N = KV ? per_head * p.G : per_head;   // stream tiles
 
-  if (warp == 8) {
-    // ------------------------------------------------------------ loads
-    if (lane == 0 && N > 0) {
-      tma_prefetch_desc(&tm_x1);
-      tma_prefetch_desc(&tm_x2);
-      tma_prefetch_desc(&tm_y1);
-      tma_prefetch_desc(&tm_y2);
-      mbar_arrive_expect_tx(x_full, 2 * Cfg::X_B);
-      Tile::load(sx, &tm_x1, x_full, x0, hx, b, 128);
-      Tile::load(sx + Cfg::X_B, &tm_x2, x_full, x0, hx, b, 128);
-      for (int n = 0; n < N; ++n) {
-        const int st = n % NST;
-        if (n >= NST && !mbar_wait(y_empty + st, (n / NST - 1) & 1, wc)) break;
-        const int g = KV ? n / per_head : 0, row = (t_lo + n - g * per_head) * T;
-        const int hy = KV ? hx * p.G + g : hx / p.G;
-        mbar_arrive_expect_tx(y_full + st, 2 * Cfg::Y_B + (KV ? T * 16 : 0));
-        Tile::load(sy + 2 * st * Cfg::Y_B, &tm_y1, y_full + st, row, hy, b, T);
-        Tile::load(sy + (2 * st + 1) * Cfg::Y_B, &tm_y2, y_full + st, row, hy, b, T);
-        if (KV)
-          bulk_load(sr + st * Cfg::R_B, bp.rows + (static_cast<long>(b) * p.Hq + hy) * bp.rows_pad + row, T * 16,
-                    y_full + st);
-        last_load[st] = n;
-      }
-    }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ MMAs
-    if (N > 0) {   // the whole warp, converged
-      const uint32_t idesc_s = idesc_bf16_f32(128, T, false, false);
-      const uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
-      const uint64_t x1 = Tile::desc_k(sx), x2 = Tile::desc_k(sx + Cfg::X_B);
-      const uint64_t y_k = Tile::desc_k(sy), y_mn = Tile::desc_mn(sy, T);
-      constexpr uint64_t TILE = Cfg::Y_B >> 4;
-      auto issue_scores = [&](int n) -> bool {
-        const int st = n % NST;
-        if (!mbar_wait_warp(y_full + st, (n / NST) & 1, wc)) return false;
-        tc_fence_after();
-        const uint32_t col = tmem + Cfg::COL_S + (n & 1) * 2 * T;
-        const uint64_t y1 = y_k + 2 * st * TILE, y2 = y1 + TILE;
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_ss(col, x1 + Tile::kstep_k(kk, 128), y1 + Tile::kstep_k(kk, T), idesc_s, kk > 0 ? 1u : 0u);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_ss(col + T, x2 + Tile::kstep_k(kk, 128), y2 + Tile::kstep_k(kk, T), idesc_s, kk > 0 ? 1u : 0u);
-          umma_commit(s_full + (n & 1));
+  if (warp >= 8) {
+    if constexpr (Cfg::WIDE) setmaxnreg_dec<Cfg::LESS>();
+    if (warp == 8) {
+      // ------------------------------------------------------------ loads
+      if (lane == 0 && N > 0) {
+        tma_prefetch_desc(&tm_x1);
+        tma_prefetch_desc(&tm_x2);
+        tma_prefetch_desc(&tm_y1);
+        tma_prefetch_desc(&tm_y2);
+        mbar_arrive_expect_tx(x_full, 2 * Cfg::X_B);
+        Tile::load(sx, &tm_x1, x_full, x0, hx, b, 128);
+        Tile::load(sx + Cfg::X_B, &tm_x2, x_full, x0, hx, b, 128);
+        for (int n = 0; n < N; ++n) {
+          const int st = n % NST;
+          if (n >= NST && !mbar_wait(y_empty + st, (n / NST - 1) & 1, wc)) break;
+          const int g = KV ? n / per_head : 0, row = (t_lo + n - g * per_head) * T;
+          const int hy = KV ? hx * p.G + g : hx / p.G;
+          mbar_arrive_expect_tx(y_full + st, 2 * Cfg::Y_B + (KV ? Cfg::R_B : 0));
+          Tile::load(sy + 2 * st * Cfg::Y_B, &tm_y1, y_full + st, row, hy, b, T);
+          Tile::load(sy + (2 * st + 1) * Cfg::Y_B, &tm_y2, y_full + st, row, hy, b, T);
+          if (KV)
+            bulk_load(sr + st * Cfg::R_B, bp.rows + ((static_cast<long>(b) * p.Hq + hy) * bp.row_blocks + row / T) *
+                      (kAttnRowFields * T), Cfg::R_B, y_full + st);
+          last_load[st] = n;
         }
-        __syncwarp();
-        return true;
-      };
-      bool ok = mbar_wait_warp(x_full, 0, wc) && issue_scores(0);
-      if (ok && N > 1) ok = issue_scores(1);
-      for (int n = 0; ok && n < N; ++n) {
-        const int st = n % NST;
-        if (!mbar_wait_warp(p_full + (n & 1), (n >> 1) & 1, wc)) break;
-        tc_fence_after();
-        const uint32_t col = tmem + Cfg::COL_S + (n & 1) * 2 * T;
-        const uint64_t y1 = y_mn + 2 * st * TILE, y2 = y1 + TILE;
-        if (elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < T / 16; ++ks)
-            umma_ts(tmem + Cfg::COL_OUT1, col + T + ks * 8, y1 + ks * Tile::KSTEP_MN, idesc_o, (n > 0 || ks > 0) ? 1u : 0u);
-          if (KV) {
-#pragma unroll
-            for (int ks = 0; ks < T / 16; ++ks)
-              umma_ts(tmem + Cfg::COL_OUT2, col + ks * 8, y2 + ks * Tile::KSTEP_MN, idesc_o, (n > 0 || ks > 0) ? 1u : 0u);
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ MMAs
+      if (N > 0) {   // the whole warp, converged
+        const uint32_t idesc_s = idesc_bf16_f32(128, T, false, false);
+        const uint32_t idesc_o = idesc_bf16_f32(128, D, false, true);
+        const uint64_t x1 = Tile::desc_k(sx), x2 = Tile::desc_k(sx + Cfg::X_B);
+        const uint64_t y_k = Tile::desc_k(sy), y_mn = Tile::desc_mn(sy, T);
+        constexpr uint64_t TILE = Cfg::Y_B >> 4;
+        auto issue_scores = [&](int n) -> bool {
+          const int st = n % NST;
+          if (!mbar_wait_warp(y_full + st, (n / NST) & 1, wc)) return false;
+          tc_fence_after();
+          const uint32_t col = tmem + Cfg::COL_S + (n & 1) * 2 * T;
+          const uint64_t y1 = y_k + 2 * st * TILE, y2 = y1 + TILE;
+          if (elect_one()) {
+  #pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_ss(col, x1 + Tile::kstep_k(kk, 128), y1 + Tile::kstep_k(kk, T), idesc_s, kk > 0 ? 1u : 0u);
+  #pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_ss(col + T, x2 + Tile::kstep_k(kk, 128), y2 + Tile::kstep_k(kk, T), idesc_s, kk > 0 ? 1u : 0u);
+            umma_commit(s_full + (n & 1));
           }
-          umma_commit(y_empty + st);
+          __syncwarp();
+          return true;
+        };
+        bool ok = mbar_wait_warp(x_full, 0, wc) && issue_scores(0);
+        if (ok && N > 1) ok = issue_scores(1);
+        for (int n = 0; ok && n < N; ++n) {
+          const int st = n % NST;
+          if (!mbar_wait_warp(p_full + (n & 1), (n >> 1) & 1, wc)) break;
+          tc_fence_after();
+          const uint32_t col = tmem + Cfg::COL_S + (n & 1) * 2 * T;
+          const uint64_t y1 = y_mn + 2 * st * TILE, y2 = y1 + TILE;
+          if (elect_one()) {
+  #pragma unroll
+            for (int ks = 0; ks < T / 16; ++ks)
+              umma_ts(tmem + Cfg::COL_OUT1, col + T + ks * 8, y1 + ks * Tile::KSTEP_MN, idesc_o, (n > 0 || ks > 0) ? 1u : 0u);
+  #pragma unroll
+            for (int ks = 0; ks < T / 16; ++ks) {
+              if (KV)
+                umma_ts(tmem + Cfg::COL_OUT2, col + ks * 8, y2 + ks * Tile::KSTEP_MN, idesc_o, (n > 0 || ks > 0) ? 1u : 0u);
+              else   // the low parts of dS
+                umma_ts(tmem + Cfg::COL_OUT1, col + ks * 8, y1 + ks * Tile::KSTEP_MN, idesc_o, 1u);
+            }
+            umma_commit(y_empty + st);
+          }
+          __syncwarp();
+          if (n + 2 < N) ok = issue_scores(n + 2);
         }
+        if (elect_one()) umma_commit(all_done);
         __syncwarp();
-        if (n + 2 < N) ok = issue_scores(n + 2);
+        mbar_wait_drain(all_done, 0, p.timeout_ns);
+        __syncwarp();
       }
-      if (elect_one()) umma_commit(all_done);
-      __syncwarp();
-      mbar_wait_drain(all_done, 0, p.timeout_ns);
-      __syncwarp();
     }
   } else {
+    if constexpr (Cfg::WIDE) setmaxnreg_inc<Cfg::MORE>();
     // ------------------------------------------------------------ softmax
     const int w = warp >> 2, wq = warp & 3;
     const int tid = threadIdx.x & 127;
@@ -222,20 +244,27 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     const uint32_t col_s = lane_base + Cfg::COL_S + w * 2 * T, col_g = col_s + T;
     const ScoreOps ops(p.scale, p.cap, false);
+    const bool capped = MOD == 1 || (MOD == 2 && p.cap > 0.f);
     // dQ pass: this row's statistics
-    AttnRow mine{INFINITY, 0.f, 0, 0};
-    float slope2 = 0.f;
-    int pos = 0;
+    float nl2 = -INFINITY, ndelta = 0.f, slope2 = 0.f;
+    int lo = 0, hi = 0, pos = 0;
+    float* stat = bp.rows + ((static_cast<long>(b) * p.Hq + hx) * bp.row_blocks + row / T) * (kAttnRowFields * T) + row % T;
     if (!KV) {
-      if (row < p.mask.Nq) mine = bp.rows[(static_cast<long>(b) * p.Hq + hx) * bp.rows_pad + row];
-      pos = bias_position(mask, row, make_int2(mine.lo, mine.hi));
-      if (MOD && p.slopes) slope2 = p.slopes[hx] * kLog2e;
+      if (row < p.mask.Nq) {
+        nl2 = stat[0];
+        ndelta = stat[T];
+        lo = __float_as_int(stat[2 * T]);
+        hi = __float_as_int(stat[3 * T]);
+        pos = __float_as_int(stat[4 * T]);
+      }
+      if (MOD == 2) slope2 = p.slopes[hx] * kLog2e;
     }
+    uint64_t delta2 = f2_dup(0.f), total2 = delta2;  // dQ pass: sums of P g and of P
     bool ok = true;
     for (int n = w; n < N; n += 2) {
       const int st = n % NST;
       const int g = KV ? n / per_head : 0, y0 = (t_lo + n - g * per_head) * T;
-      if (KV && MOD && p.slopes) slope2 = p.slopes[hx * p.G + g] * kLog2e;
+      if (KV && MOD == 2) slope2 = p.slopes[hx * p.G + g] * kLog2e;
       bool dead = false;                            // the streamed row this thread answers for takes no part
       if (!KV && tid < T && y0 + tid < mask.nk) {
         dead = y0 + tid >= mask.len;
@@ -246,66 +275,124 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
       }
       if (!mbar_wait_warp(s_full + w, (n >> 1) & 1, wc)) { ok = false; break; }
       tc_fence_after();
-      const AttnRow* rs = reinterpret_cast<const AttnRow*>(sr + st * Cfg::R_B);
+      const float* rs = reinterpret_cast<const float*>(sr + st * Cfg::R_B);
+      const int* ri = reinterpret_cast<const int*>(rs);
       bool full;
       if (KV) {
         // the statistics came with the tile; waiting here makes them visible to this thread
         if (!mbar_wait_warp(y_full + st, (n / NST) & 1, wc)) { ok = false; break; }
-        full = y0 + T <= mask.qlen && rs[0].hi >= x0 + 128 && rs[T - 1].lo <= x0;
-        dead = tid < T && rs[tid].l2 == INFINITY;
+        full = y0 + T <= mask.qlen && ri[3 * T] >= x0 + 128 && ri[3 * T - 1] <= x0;
+        dead = tid < T && rs[tid] == -INFINITY;
       } else {
-        full = __all_sync(~0u, mine.lo <= y0 && mine.hi >= y0 + T);
+        full = __all_sync(~0u, lo <= y0 && hi >= y0 + T);
       }
+      // dQ pass, bias: side 1 (-1) where every row of the warp stands behind (before) all keys of the tile
+      const int side = KV || MOD != 2 ? 0 : __all_sync(~0u, pos >= y0 + T - 1) ? 1 : __all_sync(~0u, pos <= y0) ? -1 : 0;
+      uint32_t s[2][CH], gg[2][CH];
+      tmem_ld_cols<CH>(col_s, s[0]);
+      tmem_ld_cols<CH>(col_g, gg[0]);
+      tmem_wait_ld();
+      regs_loaded(s[0]);
+      regs_loaded(gg[0]);
 #pragma unroll
       for (int c = 0; c < T; c += CH) {
-        uint32_t s[CH], gg[CH], pk[CH / 2], dk[CH / 2];
-        tmem_ld_cols<CH>(col_s + c, s);
-        tmem_ld_cols<CH>(col_g + c, gg);
-        tmem_wait_ld();
-        regs_loaded(s);
-        regs_loaded(gg);
+        constexpr int NB = CH;
+        const int cur = (c / CH) & 1;
+        if (c + CH < T) {   // the next columns' read in flight
+          tmem_ld_cols<NB>(col_s + c + CH, s[cur ^ 1]);
+          tmem_ld_cols<NB>(col_g + c + CH, gg[cur ^ 1]);
+        }
+        uint32_t pk[CH / 2], dk[CH / 2], dl[CH / 2];
+        const bool small = (MOD == 1 || capped) && MOD != 0 &&
+                           __all_sync(~0u, ops.small(fmaxf(max_of(s[cur]), -min_of(s[cur]))));
+        // x - l2 of the columns, and 1 - tanh^2
+        uint64_t x[CH / 2], dx[CH / 2];
 #pragma unroll
-        for (int k = 0; k < CH; k += 2) {
-          float pv[2], dv[2];
+        for (int q = 0; q < CH / 2; ++q) x[q] = f2(s[cur][2 * q], s[cur][2 * q + 1]);
+        if (MOD == 1 || (MOD == 2 && capped)) {
+          if (small) {
+#pragma unroll
+            for (int q = 0; q < CH / 2; ++q) x[q] = ops.poly(x[q], f2_dup(0.f));
+          } else {
+#pragma unroll
+            for (int q = 0; q < CH / 2; ++q)
+              x[q] = f2_pack(ops.tanh_any(as_f(s[cur][2 * q])), ops.tanh_any(as_f(s[cur][2 * q + 1])));
+          }
+#pragma unroll
+          for (int q = 0; q < CH / 2; ++q) dx[q] = f2_fma(f2_mul(x[q], f2_dup(-1.f)), x[q], f2_dup(1.f));
+        }
+        const uint64_t f = f2_dup(capped ? ops.out : ops.c2);
+        uint64_t b2 = f2_dup(0.f), step = b2;
+        if (MOD == 2 && !KV && side != 0) step = f2_dup(side > 0 ? 2.f * slope2 : -2.f * slope2);
+#pragma unroll
+        for (int q = 0; q < CH / 2; q += 2) {
+          float4 l4 = make_float4(nl2, nl2, nl2, nl2), d4 = make_float4(ndelta, ndelta, ndelta, ndelta);
+          if (KV) {
+            l4 = *reinterpret_cast<const float4*>(rs + c + 2 * q);
+            d4 = *reinterpret_cast<const float4*>(rs + T + c + 2 * q);
+          }
+          const uint64_t ll[2] = {f2_pack(l4.x, l4.y), f2_pack(l4.z, l4.w)};
+          const uint64_t dd[2] = {f2_pack(d4.x, d4.y), f2_pack(d4.z, d4.w)};
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const int y = c + k + u;
-            float l2 = mine.l2, delta = mine.delta;
-            if (KV) {
-              l2 = rs[y].l2;
-              delta = rs[y].delta;
-            }
-            float x = __uint_as_float(s[k + u]) * ops.c2, dx = 1.f;
-            if (MOD && p.cap > 0.f) {
-              x = ops.capped(__uint_as_float(s[k + u]));
-              const float t = x / ops.out;
-              dx = fmaf(-t, t, 1.f);
-            }
-            if (MOD && p.slopes) {
-              int d;
+            const int k = c + 2 * (q + u);           // the pair's first column
+            uint64_t t = f2_fma(x[q + u], f, ll[u]);
+            if (MOD == 2) {
               if (KV) {
-                const int2 iv = make_int2(rs[y].lo, rs[y].hi);
-                d = bias_position(mask, y0 + y, iv) - row;
+                t = f2_add(t, f2_pack(-slope2 * fabsf(static_cast<float>(ri[4 * T + k] - row)),
+                                      -slope2 * fabsf(static_cast<float>(ri[4 * T + k + 1] - row))));
               } else {
-                d = pos - (y0 + y);
+                const float d = static_cast<float>(pos - y0);
+                if (side != 0) {
+                  if ((q + u) % 8 == 0) {
+                    const float gs = side > 0 ? -slope2 : slope2;
+                    b2 = f2_pack(gs * (d - k), gs * (d - (k + 1)));
+                  }
+                  t = f2_add(t, b2);
+                  b2 = f2_add(b2, step);
+                } else {
+                  t = f2_add(t, f2_pack(-slope2 * fabsf(d - k), -slope2 * fabsf(d - (k + 1))));
+                }
               }
-              x = fmaf(-slope2, fabsf(static_cast<float>(d)), x);
             }
-            float pr = ex2_mufu(x - l2);
-            float ds = pr * (__uint_as_float(gg[k + u]) - delta);
-            if (MOD) ds *= dx;
+            float p0, p1;
+            ex2_pair(t, p0, p1);
+            uint64_t pp = f2_pack(p0, p1);
+            uint64_t pg = f2_mul(pp, f2(gg[cur][2 * (q + u)], gg[cur][2 * (q + u) + 1]));
+            uint64_t ds = f2_fma(pp, dd[u], pg);     // P (g - delta)
+            if (MOD == 1 || (MOD == 2 && capped)) ds = f2_mul(ds, dx[q + u]);
             if (!full) {
-              const int lo = KV ? rs[y].lo : mine.lo, hi = KV ? rs[y].hi : mine.hi, key = KV ? row : y0 + y;
-              if (key < lo || key >= hi) pr = ds = 0.f;
+              float a0, a1, b0, b1;
+              f2_unpack(ds, a0, a1);
+              f2_unpack(pg, b0, b1);
+              const bool h0 = KV ? row < ri[2 * T + k] || row >= ri[3 * T + k] : y0 + k < lo || y0 + k >= hi;
+              const bool h1 = KV ? row < ri[2 * T + k + 1] || row >= ri[3 * T + k + 1] : y0 + k + 1 < lo || y0 + k + 1 >= hi;
+              p0 = h0 ? 0.f : p0;
+              p1 = h1 ? 0.f : p1;
+              ds = f2_pack(h0 ? 0.f : a0, h1 ? 0.f : a1);
+              pg = f2_pack(h0 ? 0.f : b0, h1 ? 0.f : b1);
             }
-            pv[u] = pr;
-            dv[u] = ds;
+            float s0, s1;
+            f2_unpack(ds, s0, s1);
+            const uint32_t hi16 = pack_bf16x2(s0, s1);
+            dk[q + u] = hi16;
+            if (KV) {
+              pk[q + u] = pack_bf16x2(p0, p1);
+            } else {
+              delta2 = f2_add(delta2, pg);
+              total2 = f2_add(total2, f2_pack(p0, p1));
+              f2_unpack(f2_fma(f2_pack(bf16_lo(hi16), bf16_hi(hi16)), f2_dup(-1.f), ds), s0, s1);
+              dl[q + u] = pack_bf16x2(s0, s1);
+            }
           }
-          pk[k / 2] = pack_bf16x2(pv[0], pv[1]);
-          dk[k / 2] = pack_bf16x2(dv[0], dv[1]);
         }
-        if (KV) tmem_st_cols<CH / 2>(col_s + c / 2, pk);
+        tmem_st_cols<CH / 2>(col_s + c / 2, KV ? pk : dl);
         tmem_st_cols<CH / 2>(col_g + c / 2, dk);
+        if (c + CH < T) {
+          tmem_wait_ld();
+          regs_loaded(s[cur ^ 1]);
+          regs_loaded(gg[cur ^ 1]);
+        }
       }
       if (dead) {
         if (!mbar_wait(y_full + st, (n / NST) & 1, wc)) ok = false;   // landed before the scores were computed
@@ -318,6 +405,22 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
       tc_fence_before();
       mbar_arrive_warp(p_full + w);
     }
+    float inv_total = 1.f;
+    if (!KV) {   // both warpgroups' shares; delta and l2 as they come out, for the dK/dV pass
+      float d0, d1, t0, t1;
+      f2_unpack(delta2, d0, d1);
+      f2_unpack(total2, t0, t1);
+      float2* share = reinterpret_cast<float2*>(sr);
+      share[w * 128 + tid] = make_float2(d0 + d1, t0 + t1);
+      named_bar_sync(1, 256);
+      const float2 a = share[tid], c = share[128 + tid];
+      const float total = a.y + c.y;
+      inv_total = total > 0.f ? 1.f / total : total;   // NaN stays
+      if (w == 0 && row < p.mask.Nq && nl2 != -INFINITY) {
+        stat[0] = nl2 - log2f(total);
+        stat[T] = -(a.x + c.x) * inv_total;
+      }
+    }
     if (ok && N > 0) ok = mbar_wait_warp(all_done, 0, wc);
     ok = __all_sync(~0u, ok);
     if (ok) {
@@ -329,11 +432,11 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
       uint16_t* out = second ? bp.dv + b * bp.dvs[0] + hx * bp.dvs[1] + static_cast<long>(row) * bp.dvs[2]
                       : KV   ? bp.dk + b * bp.dks[0] + hx * bp.dks[1] + static_cast<long>(row) * bp.dks[2]
                              : bp.dq + b * bp.dqs[0] + hx * bp.dqs[1] + static_cast<long>(row) * bp.dqs[2];
-      const float f = second ? 1.f : p.scale;
+      const float f = second ? 1.f : p.scale * inv_total;
       const bool have = row < (KV ? p.mask.Nk : p.mask.Nq);
       // a row that takes no part gets zeros, whatever its lane holds
       const bool zero = N == 0 || (KV ? row >= mask.len || (mask.doc && have && mask.doc[row].x == mask.doc[row].y)
-                                      : mine.l2 == INFINITY);
+                                      : nl2 == -INFINITY);
       for (int d = d_beg; d < d_end; d += 16) {
         uint32_t o[16];
         if (N > 0) {
@@ -380,12 +483,12 @@ cudaError_t launch_attn_bwd_pass(const CUtensorMap& x1, const CUtensorMap& x2, c
     kern<<<grid, threads, smem, s>>>(x1, x2, y1, y2, p);
     return cudaGetLastError();
   };
-  const bool mod = p.a.cap > 0.f || p.a.slopes;
   auto by_mod = [&](auto d) {
     constexpr int D = decltype(d)::value;
     using C = BwdCfg<D>;
-    return mod ? go(attn_bwd_kernel<D, KV, true>, C::BYTES, C::THREADS, C::CTAS)
-               : go(attn_bwd_kernel<D, KV, false>, C::BYTES, C::THREADS, C::CTAS);
+    return p.a.slopes      ? go(attn_bwd_kernel<D, KV, 2>, C::BYTES, C::THREADS, C::CTAS)
+           : p.a.cap > 0.f ? go(attn_bwd_kernel<D, KV, 1>, C::BYTES, C::THREADS, C::CTAS)
+                           : go(attn_bwd_kernel<D, KV, 0>, C::BYTES, C::THREADS, C::CTAS);
   };
   switch (p.a.D) {
     case 16: return by_mod(std::integral_constant<int, 16>{});
