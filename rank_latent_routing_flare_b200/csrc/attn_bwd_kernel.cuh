@@ -40,6 +40,8 @@
 // SM; the exponentials bound those.
 #pragma once
 
+#include <type_traits>
+
 #include "attn_common.cuh"
 
 namespace flare {
@@ -273,13 +275,11 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
           dead |= d.x == d.y;
         }
       }
-      if (!mbar_wait_warp(s_full + w, (n >> 1) & 1, wc)) { ok = false; break; }
-      tc_fence_after();
       const float* rs = reinterpret_cast<const float*>(sr + st * Cfg::R_B);
       const int* ri = reinterpret_cast<const int*>(rs);
       bool full;
       if (KV) {
-        // the statistics came with the tile; waiting here makes them visible to this thread
+        // the statistics come with the tile; waiting for it makes them visible to this thread
         if (!mbar_wait_warp(y_full + st, (n / NST) & 1, wc)) { ok = false; break; }
         full = y0 + T <= mask.qlen && ri[3 * T] >= x0 + 128 && ri[3 * T - 1] <= x0;
         dead = tid < T && rs[tid] == -INFINITY;
@@ -288,112 +288,120 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
       }
       // dQ pass, bias: side 1 (-1) where every row of the warp stands behind (before) all keys of the tile
       const int side = KV || MOD != 2 ? 0 : __all_sync(~0u, pos >= y0 + T - 1) ? 1 : __all_sync(~0u, pos <= y0) ? -1 : 0;
-      uint32_t s[2][CH], gg[2][CH];
-      tmem_ld_cols<CH>(col_s, s[0]);
-      tmem_ld_cols<CH>(col_g, gg[0]);
-      tmem_wait_ld();
-      regs_loaded(s[0]);
-      regs_loaded(gg[0]);
-#pragma unroll
-      for (int c = 0; c < T; c += CH) {
-        constexpr int NB = CH;
-        const int cur = (c / CH) & 1;
-        if (c + CH < T) {   // the next columns' read in flight
-          tmem_ld_cols<NB>(col_s + c + CH, s[cur ^ 1]);
-          tmem_ld_cols<NB>(col_g + c + CH, gg[cur ^ 1]);
-        }
-        uint32_t pk[CH / 2], dk[CH / 2], dl[CH / 2];
-        const bool small = (MOD == 1 || capped) && MOD != 0 &&
-                           __all_sync(~0u, ops.small(fmaxf(max_of(s[cur]), -min_of(s[cur]))));
-        // x - l2 of the columns, and 1 - tanh^2
-        uint64_t x[CH / 2], dx[CH / 2];
-#pragma unroll
-        for (int q = 0; q < CH / 2; ++q) x[q] = f2(s[cur][2 * q], s[cur][2 * q + 1]);
-        if (MOD == 1 || (MOD == 2 && capped)) {
-          if (small) {
-#pragma unroll
-            for (int q = 0; q < CH / 2; ++q) x[q] = ops.poly(x[q], f2_dup(0.f));
-          } else {
-#pragma unroll
-            for (int q = 0; q < CH / 2; ++q)
-              x[q] = f2_pack(ops.tanh_any(as_f(s[cur][2 * q])), ops.tanh_any(as_f(s[cur][2 * q + 1])));
+      if (!mbar_wait_warp(s_full + w, (n >> 1) & 1, wc)) { ok = false; break; }
+      tc_fence_after();
+      // one body for tiles that every row sees whole, one for the others
+      auto tile = [&](auto whole) {
+        constexpr bool FULL = decltype(whole)::value;
+        uint32_t s[2][CH], gg[2][CH];
+        tmem_ld_cols<CH>(col_s, s[0]);
+        tmem_ld_cols<CH>(col_g, gg[0]);
+        tmem_wait_ld();
+        regs_loaded(s[0]);
+        regs_loaded(gg[0]);
+  #pragma unroll
+        for (int c = 0; c < T; c += CH) {
+          constexpr int NB = CH;
+          const int cur = (c / CH) & 1;
+          if (c + CH < T) {   // the next columns' read in flight
+            tmem_ld_cols<NB>(col_s + c + CH, s[cur ^ 1]);
+            tmem_ld_cols<NB>(col_g + c + CH, gg[cur ^ 1]);
           }
-#pragma unroll
-          for (int q = 0; q < CH / 2; ++q) dx[q] = f2_fma(f2_mul(x[q], f2_dup(-1.f)), x[q], f2_dup(1.f));
-        }
-        const uint64_t f = f2_dup(capped ? ops.out : ops.c2);
-        uint64_t b2 = f2_dup(0.f), step = b2;
-        if (MOD == 2 && !KV && side != 0) step = f2_dup(side > 0 ? 2.f * slope2 : -2.f * slope2);
-#pragma unroll
-        for (int q = 0; q < CH / 2; q += 2) {
-          float4 l4 = make_float4(nl2, nl2, nl2, nl2), d4 = make_float4(ndelta, ndelta, ndelta, ndelta);
-          if (KV) {
-            l4 = *reinterpret_cast<const float4*>(rs + c + 2 * q);
-            d4 = *reinterpret_cast<const float4*>(rs + T + c + 2 * q);
+          uint32_t pk[CH / 2], dk[CH / 2], dl[CH / 2];
+          const bool small = (MOD == 1 || capped) && MOD != 0 &&
+                             __all_sync(~0u, ops.small(fmaxf(max_of(s[cur]), -min_of(s[cur]))));
+          // x - l2 of the columns, and 1 - tanh^2
+          uint64_t x[CH / 2], dx[CH / 2];
+  #pragma unroll
+          for (int q = 0; q < CH / 2; ++q) x[q] = f2(s[cur][2 * q], s[cur][2 * q + 1]);
+          if (MOD == 1 || (MOD == 2 && capped)) {
+            if (small) {
+  #pragma unroll
+              for (int q = 0; q < CH / 2; ++q) x[q] = ops.poly(x[q], f2_dup(0.f));
+            } else {
+  #pragma unroll
+              for (int q = 0; q < CH / 2; ++q)
+                x[q] = f2_pack(ops.tanh_any(as_f(s[cur][2 * q])), ops.tanh_any(as_f(s[cur][2 * q + 1])));
+            }
+  #pragma unroll
+            for (int q = 0; q < CH / 2; ++q) dx[q] = f2_fma(f2_mul(x[q], f2_dup(-1.f)), x[q], f2_dup(1.f));
           }
-          const uint64_t ll[2] = {f2_pack(l4.x, l4.y), f2_pack(l4.z, l4.w)};
-          const uint64_t dd[2] = {f2_pack(d4.x, d4.y), f2_pack(d4.z, d4.w)};
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int k = c + 2 * (q + u);           // the pair's first column
-            uint64_t t = f2_fma(x[q + u], f, ll[u]);
-            if (MOD == 2) {
-              if (KV) {
-                t = f2_add(t, f2_pack(-slope2 * fabsf(static_cast<float>(ri[4 * T + k] - row)),
-                                      -slope2 * fabsf(static_cast<float>(ri[4 * T + k + 1] - row))));
-              } else {
-                const float d = static_cast<float>(pos - y0);
-                if (side != 0) {
-                  if ((q + u) % 8 == 0) {
-                    const float gs = side > 0 ? -slope2 : slope2;
-                    b2 = f2_pack(gs * (d - k), gs * (d - (k + 1)));
-                  }
-                  t = f2_add(t, b2);
-                  b2 = f2_add(b2, step);
+          const uint64_t f = f2_dup(capped ? ops.out : ops.c2);
+          uint64_t b2 = f2_dup(0.f), step = b2;
+          if (MOD == 2 && !KV && side != 0) step = f2_dup(side > 0 ? 2.f * slope2 : -2.f * slope2);
+  #pragma unroll
+          for (int q = 0; q < CH / 2; q += 2) {
+            float4 l4 = make_float4(nl2, nl2, nl2, nl2), d4 = make_float4(ndelta, ndelta, ndelta, ndelta);
+            if (KV) {
+              l4 = *reinterpret_cast<const float4*>(rs + c + 2 * q);
+              d4 = *reinterpret_cast<const float4*>(rs + T + c + 2 * q);
+            }
+            const uint64_t ll[2] = {f2_pack(l4.x, l4.y), f2_pack(l4.z, l4.w)};
+            const uint64_t dd[2] = {f2_pack(d4.x, d4.y), f2_pack(d4.z, d4.w)};
+  #pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int k = c + 2 * (q + u);           // the pair's first column
+              uint64_t t = f2_fma(x[q + u], f, ll[u]);
+              if (MOD == 2) {
+                if (KV) {
+                  t = f2_add(t, f2_pack(-slope2 * fabsf(static_cast<float>(ri[4 * T + k] - row)),
+                                        -slope2 * fabsf(static_cast<float>(ri[4 * T + k + 1] - row))));
                 } else {
-                  t = f2_add(t, f2_pack(-slope2 * fabsf(d - k), -slope2 * fabsf(d - (k + 1))));
+                  const float d = static_cast<float>(pos - y0);
+                  if (side != 0) {
+                    if ((q + u) % 8 == 0) {
+                      const float gs = side > 0 ? -slope2 : slope2;
+                      b2 = f2_pack(gs * (d - k), gs * (d - (k + 1)));
+                    }
+                    t = f2_add(t, b2);
+                    b2 = f2_add(b2, step);
+                  } else {
+                    t = f2_add(t, f2_pack(-slope2 * fabsf(d - k), -slope2 * fabsf(d - (k + 1))));
+                  }
                 }
               }
-            }
-            float p0, p1;
-            ex2_pair(t, p0, p1);
-            uint64_t pp = f2_pack(p0, p1);
-            uint64_t pg = f2_mul(pp, f2(gg[cur][2 * (q + u)], gg[cur][2 * (q + u) + 1]));
-            uint64_t ds = f2_fma(pp, dd[u], pg);     // P (g - delta)
-            if (MOD == 1 || (MOD == 2 && capped)) ds = f2_mul(ds, dx[q + u]);
-            if (!full) {
-              float a0, a1, b0, b1;
-              f2_unpack(ds, a0, a1);
-              f2_unpack(pg, b0, b1);
-              const bool h0 = KV ? row < ri[2 * T + k] || row >= ri[3 * T + k] : y0 + k < lo || y0 + k >= hi;
-              const bool h1 = KV ? row < ri[2 * T + k + 1] || row >= ri[3 * T + k + 1] : y0 + k + 1 < lo || y0 + k + 1 >= hi;
-              p0 = h0 ? 0.f : p0;
-              p1 = h1 ? 0.f : p1;
-              ds = f2_pack(h0 ? 0.f : a0, h1 ? 0.f : a1);
-              pg = f2_pack(h0 ? 0.f : b0, h1 ? 0.f : b1);
-            }
-            float s0, s1;
-            f2_unpack(ds, s0, s1);
-            const uint32_t hi16 = pack_bf16x2(s0, s1);
-            dk[q + u] = hi16;
-            if (KV) {
-              pk[q + u] = pack_bf16x2(p0, p1);
-            } else {
-              delta2 = f2_add(delta2, pg);
-              total2 = f2_add(total2, f2_pack(p0, p1));
-              f2_unpack(f2_fma(f2_pack(bf16_lo(hi16), bf16_hi(hi16)), f2_dup(-1.f), ds), s0, s1);
-              dl[q + u] = pack_bf16x2(s0, s1);
+              float p0, p1;
+              ex2_pair(t, p0, p1);
+              uint64_t pp = f2_pack(p0, p1);
+              uint64_t pg = f2_mul(pp, f2(gg[cur][2 * (q + u)], gg[cur][2 * (q + u) + 1]));
+              uint64_t ds = f2_fma(pp, dd[u], pg);     // P (g - delta)
+              if (MOD == 1 || (MOD == 2 && capped)) ds = f2_mul(ds, dx[q + u]);
+              if (!FULL) {
+                float a0, a1, b0, b1;
+                f2_unpack(ds, a0, a1);
+                f2_unpack(pg, b0, b1);
+                const bool h0 = KV ? row < ri[2 * T + k] || row >= ri[3 * T + k] : y0 + k < lo || y0 + k >= hi;
+                const bool h1 = KV ? row < ri[2 * T + k + 1] || row >= ri[3 * T + k + 1] : y0 + k + 1 < lo || y0 + k + 1 >= hi;
+                p0 = h0 ? 0.f : p0;
+                p1 = h1 ? 0.f : p1;
+                ds = f2_pack(h0 ? 0.f : a0, h1 ? 0.f : a1);
+                pg = f2_pack(h0 ? 0.f : b0, h1 ? 0.f : b1);
+              }
+              float s0, s1;
+              f2_unpack(ds, s0, s1);
+              const uint32_t hi16 = pack_bf16x2(s0, s1);
+              dk[q + u] = hi16;
+              if (KV) {
+                pk[q + u] = pack_bf16x2(p0, p1);
+              } else {
+                delta2 = f2_add(delta2, pg);
+                total2 = f2_add(total2, f2_pack(p0, p1));
+                f2_unpack(f2_fma(f2_pack(bf16_lo(hi16), bf16_hi(hi16)), f2_dup(-1.f), ds), s0, s1);
+                dl[q + u] = pack_bf16x2(s0, s1);
+              }
             }
           }
+          tmem_st_cols<CH / 2>(col_s + c / 2, KV ? pk : dl);
+          tmem_st_cols<CH / 2>(col_g + c / 2, dk);
+          if (c + CH < T) {
+            tmem_wait_ld();
+            regs_loaded(s[cur ^ 1]);
+            regs_loaded(gg[cur ^ 1]);
+          }
         }
-        tmem_st_cols<CH / 2>(col_s + c / 2, KV ? pk : dl);
-        tmem_st_cols<CH / 2>(col_g + c / 2, dk);
-        if (c + CH < T) {
-          tmem_wait_ld();
-          regs_loaded(s[cur ^ 1]);
-          regs_loaded(gg[cur ^ 1]);
-        }
-      }
+      };
+      if (full) tile(std::true_type{});
+      else tile(std::false_type{});
       if (dead) {
         if (!mbar_wait(y_full + st, (n / NST) & 1, wc)) ok = false;   // landed before the scores were computed
         Tile::zero_row(sy + 2 * st * Cfg::Y_B, tid, T);
