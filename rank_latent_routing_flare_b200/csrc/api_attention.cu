@@ -59,7 +59,7 @@ AttnPlan make_attn_plan(int64_t B, int64_t Hq, int64_t Hk, int64_t Nq, int64_t N
   off += align256(static_cast<size_t>(B * Nk) * sizeof(int2));
   const size_t rows = static_cast<size_t>(B * Hq * Nq);
   if (backward) {
-    const int64_t t = attn_bwd_stream_tile(static_cast<int>(D));
+    const int64_t t = attn_bwd_stream_tile(static_cast<int>(D), true);
     pl.row_blocks = static_cast<int>(cdiv(Nq, t));
     pl.off_rows = off;
     off += align256(static_cast<size_t>(B * Hq) * pl.row_blocks * t * kAttnRowFields * 4);
@@ -212,6 +212,9 @@ flare_status flare_attention_bwd(const flare_attention_args* a, void* workspace,
   if (st == FLARE_OK) st = fill_strides(p.dks, a->dK, a->dk_stride, a->B, a->Hk, a->Nk, a->D, true);
   if (st == FLARE_OK) st = fill_strides(p.dvs, a->dV, a->dv_stride, a->B, a->Hk, a->Nk, a->D, true);
   if (st != FLARE_OK) return st;
+  p.q = AttnSide{a->Q, r.q[0], r.q[1], r.q[2]};
+  p.k = AttnSide{a->K, r.k[0], r.k[1], r.k[2]};
+  p.v = AttnSide{a->V, r.v[0], r.v[1], r.v[2]};
   p.yin = AttnSide{a->Y, ys[0], ys[1], ys[2]};
   p.dy = AttnSide{a->dY, dys[0], dys[1], dys[2]};
   p.dq = a->dQ;
@@ -222,11 +225,11 @@ flare_status flare_attention_bwd(const flare_attention_args* a, void* workspace,
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!documents(a, pl, workspace, s) || launch_attn_rows(p, s) != cudaSuccess) return FLARE_ERR_LAUNCH;
   // the dQ pass keeps tiles of 128 rows of Q and dY and streams K and V; the dK/dV pass the other way round
-  const int t = attn_bwd_stream_tile(p.a.D);
+  const int tq = attn_bwd_stream_tile(p.a.D, false), tkv = attn_bwd_stream_tile(p.a.D, true);
   AttnMaps dq, dkv;
   if (!map_rows(&dq.q, a->Q, r.q, a->B, a->Hq, a->Nq, a->D, 128) || !map_rows(&dq.dy, a->dY, dys, a->B, a->Hq, a->Nq, a->D, 128) ||
-      !map_rows(&dq.k, a->K, r.k, a->B, a->Hk, a->Nk, a->D, t) || !map_rows(&dq.v, a->V, r.v, a->B, a->Hk, a->Nk, a->D, t) ||
-      !map_rows(&dkv.q, a->Q, r.q, a->B, a->Hq, a->Nq, a->D, t) || !map_rows(&dkv.dy, a->dY, dys, a->B, a->Hq, a->Nq, a->D, t) ||
+      !map_rows(&dq.k, a->K, r.k, a->B, a->Hk, a->Nk, a->D, tq) || !map_rows(&dq.v, a->V, r.v, a->B, a->Hk, a->Nk, a->D, tq) ||
+      !map_rows(&dkv.q, a->Q, r.q, a->B, a->Hq, a->Nq, a->D, tkv) || !map_rows(&dkv.dy, a->dY, dys, a->B, a->Hq, a->Nq, a->D, tkv) ||
       !map_rows(&dkv.k, a->K, r.k, a->B, a->Hk, a->Nk, a->D, 128) || !map_rows(&dkv.v, a->V, r.v, a->B, a->Hk, a->Nk, a->D, 128))
     return FLARE_ERR_LAUNCH;
   if (launch_attn_bwd_dq(dq, p, s) != cudaSuccess || launch_attn_bwd_dkv(dkv, p, s) != cudaSuccess)

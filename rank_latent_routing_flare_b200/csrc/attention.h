@@ -41,7 +41,7 @@ struct AttnParams {
 };
 
 // Statistics of the backward's query rows: per batch entry and query head,
-// blocks of T = attn_bwd_stream_tile(D) rows, each kAttnRowFields arrays of T
+// blocks of T = attn_bwd_stream_tile(D, true) rows, each kAttnRowFields arrays of T
 // 4-byte values: -l2 (P = 2^(x - l2); -inf: the row sees nothing), -delta
 // (delta = <dY, Y>), the interval [lo, hi) of keys that it sees, and its
 // position for the distance bias.
@@ -49,7 +49,7 @@ constexpr int kAttnRowFields = 5;
 
 struct AttnBwdParams {
   AttnParams a;
-  AttnSide dy, yin;
+  AttnSide q, k, v, dy, yin;
   uint16_t *dq, *dk, *dv;
   long dqs[3], dks[3], dvs[3];
   float* rows;
@@ -72,7 +72,7 @@ constexpr int kAttnStepRows = 16;   // query rows per key head of the kernel for
 cudaError_t launch_attn_step(const AttnParams& p, const AttnSide& q, const AttnSide& k, const AttnSide& v,
                              cudaStream_t s);
 
-int attn_bwd_stream_tile(int D);
+int attn_bwd_stream_tile(int D, bool kv);   // rows per streamed tile of the dQ pass and of the dK/dV pass
 cudaError_t launch_attn_rows(const AttnBwdParams& p, cudaStream_t s);
 cudaError_t launch_attn_bwd_dq(const AttnMaps& m, const AttnBwdParams& p, cudaStream_t s);
 cudaError_t launch_attn_bwd_dkv(const AttnMaps& m, const AttnBwdParams& p, cudaStream_t s);

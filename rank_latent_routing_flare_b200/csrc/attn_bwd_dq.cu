@@ -10,7 +10,7 @@ namespace {
 // loads.
 template <int D>
 __global__ void __launch_bounds__(256) attn_rows_kernel(const AttnBwdParams bp) {
-  constexpr int L = D / 8, ROWS = 256 / L, T = BwdCfg<D>::T;
+  constexpr int L = D / 8, ROWS = 256 / L, T = BwdCfg<D, true>::T;
   const AttnParams& p = bp.a;
   const int rows = bp.row_blocks * T, blocks = (rows + ROWS - 1) / ROWS;
   const long bh = blockIdx.x / blocks;
@@ -48,12 +48,16 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const AttnBwdParams bp) 
 
 }  // namespace
 
-int attn_bwd_stream_tile(int D) { return D >= 64 ? BwdCfg<64>::T : BwdCfg<32>::T; }
+int attn_bwd_stream_tile(int D, bool kv) {
+  return D == 128  ? (kv ? BwdCfg<128, true>::T : BwdCfg<128, false>::T)
+         : D == 64 ? (kv ? BwdCfg<64, true>::T : BwdCfg<64, false>::T)
+                   : (kv ? BwdCfg<32, true>::T : BwdCfg<32, false>::T);
+}
 
 cudaError_t launch_attn_rows(const AttnBwdParams& p, cudaStream_t s) {
   auto go = [&](auto d) {
     constexpr int D = decltype(d)::value, ROWS = 256 / (D / 8);
-    const long blocks = (static_cast<long>(p.row_blocks) * BwdCfg<D>::T + ROWS - 1) / ROWS;
+    const long blocks = (static_cast<long>(p.row_blocks) * BwdCfg<D, true>::T + ROWS - 1) / ROWS;
     attn_rows_kernel<D><<<static_cast<unsigned>(blocks * p.a.B * p.a.Hq), 256, 0, s>>>(p);
     return cudaGetLastError();
   };

@@ -14,12 +14,13 @@
 //   dK/dV pass  rows: keys (K, V), stream: the rows (Q, dY) of every query
 //     head of the key head, S = K Q^T, G = V dY^T, out1 += dS Q, out2 += P dY
 //
-// The rows are TMEM lanes (UMMA M = 128).  The two warpgroups take stream
-// tiles in turn: each has its own S and G columns and both add to the same
-// accumulators.  Weights and dS are written over S and G as bf16 and read from
-// there as the products' A operands; the MMA warp issues tile n's products
-// and right behind them the scores of tile n + 2 into the same columns (the
-// tensor pipe runs in order), while the other warpgroup works on tile n + 1.
+// The rows are TMEM lanes (UMMA M = 128).  There are two pairs of S and G
+// columns.  Weights and dS are written over S and G as bf16 and read from there
+// as the products' A operands; the MMA warp issues tile n's products and right
+// behind them the scores of tile n + 2 into the same columns (the tensor pipe
+// runs in order), while the softmax threads work on tile n + 1.  D >= 64: four
+// warpgroups share a tile, a quarter of its columns each, so that its weights
+// are ready before the tensor pipe runs dry.  D <= 32: two take tiles in turn.
 // Row statistics (l2, delta, interval) are held in registers in the dQ pass
 // and come with the stream in the dK/dV pass.
 //
@@ -35,9 +36,8 @@
 // Streamed rows that take no part (padding) are zeroed in shared memory
 // before the products read them: a weight of 0 does not erase a NaN.
 //
-// D >= 64: T = 64, up to 512 TMEM columns, one CTA per SM whose softmax threads
-// take over most of its registers.  D <= 32: T = 48, 256 columns, two CTAs per
-// SM; the exponentials bound those.
+// D >= 64: T = 64, up to 512 TMEM columns, one CTA per SM.  D <= 32: T = 48, 256
+// columns, two CTAs per SM; the exponentials bound those.
 #pragma once
 
 #include <type_traits>
@@ -46,42 +46,52 @@
 
 namespace flare {
 
-template <int D_>
+#ifndef TKV128
+#define TKV128 64
+#endif
+template <int D_, bool KV>
 struct BwdCfg {
   static constexpr int D = D_;
   using Tile = RowTile<D>;
-  static constexpr int T = D >= 64 ? 64 : 48;
-  static constexpr int CH = D >= 64 ? 32 : 16;           // columns of a tile computed at once
-  static constexpr int CTAS = D >= 64 ? 1 : 2;
-  static constexpr int NST = D == 128 ? 4 : 6;
-  static constexpr int X_B = Tile::bytes(128), Y_B = Tile::bytes(T), R_B = kAttnRowFields * T * 4;
+  static constexpr int T = D <= 32 ? 48 : KV && D == 128 ? TKV128 : 64;
+  // Wide heads, one CTA an SM: four warpgroups share a tile, a quarter of its
+  // columns each.  Narrow ones, two CTAs an SM: two warpgroups take tiles in turn.
+  static constexpr bool SHARE = D >= 64;
+  static constexpr int CTAS = SHARE ? 1 : 2, WGS = SHARE ? 4 : 2;
+  static constexpr int COLS = SHARE ? T / WGS : T;        // columns of a tile per warpgroup
+  static constexpr int CH = 16 < COLS ? 16 : COLS;        // columns computed at once
+  static constexpr int OUTS = KV ? 2 : 1;
+  // Rows kept in TMEM, as the A operands of the score products, where columns
+  // are left: from shared memory an A operand of 128 rows takes as long to read
+  // as the product of 64 columns.
+  static constexpr bool XT = D >= 64 && 4 * T + (OUTS + 1) * D <= 512;
+  static constexpr int NST = D == 128 ? (XT ? 384 : 256) / T : 6;
+  static constexpr int X_B = XT ? 0 : Tile::bytes(128), Y_B = Tile::bytes(T), R_B = kAttnRowFields * T * 4;
   static constexpr int OFF_X = 0;                         // X1 | X2
   static constexpr int OFF_Y = OFF_X + 2 * X_B;           // NST x (Y1 | Y2)
-  static constexpr int OFF_R = OFF_Y + 2 * NST * Y_B;     // NST x row statistics (dK/dV pass)
-  static constexpr int OFF_BAR = OFF_R + NST * R_B;
+  static constexpr int OFF_R = OFF_Y + 2 * NST * Y_B;     // NST x row statistics (dK/dV pass); sums of the warpgroups (dQ pass)
+  static constexpr int OFF_BAR = OFF_R + (KV ? NST * R_B : WGS * 1024);
   static constexpr int OFF_MISC = OFF_BAR + 8 * (1 + 2 * NST + 2 + 2 + 1);
   static constexpr int BYTES = OFF_MISC + 32 + 4 * NST;
-  static constexpr uint32_t COL_S = 0, COL_OUT1 = 4 * T, COL_OUT2 = 4 * T + D;   // buffer g: S at 2 T g, G at 2 T g + T
-  static constexpr uint32_t TMEM_COLS = COL_OUT2 + D <= 256 ? 256 : 512;
-  // Warps 0-3, 4-7: softmax; 8: loads; 9: MMAs.  One CTA an SM: two more fill a
-  // third warpgroup, which gives the softmax threads its registers (168 a
-  // thread at launch).
-  static constexpr bool WIDE = CTAS == 1;
-  static constexpr int THREADS = WIDE ? 384 : 320, LESS = 56, MORE = 224;
-  static_assert(256 * MORE + 128 * LESS <= 384 * 168, "register split");
-  static_assert(COL_OUT2 + D <= TMEM_COLS && TMEM_COLS * CTAS <= 512, "TMEM columns");
-  static_assert(Y_B % (8 * Tile::ROWB) == 0 && X_B % 1024 == 0 && R_B % 64 == 0, "tiles hold whole swizzle atoms");
+  // buffer g: S at 2 T g, G at 2 T g + T
+  static constexpr uint32_t COL_S = 0, COL_OUT1 = 4 * T, COL_OUT2 = 4 * T + D, COL_X1 = 4 * T + OUTS * D, COL_X2 = COL_X1 + D / 2;
+  static constexpr uint32_t COL_END = XT ? COL_X2 + D / 2 : COL_X1;
+  static constexpr uint32_t TMEM_COLS = COL_END <= 256 ? 256 : 512;
+  static constexpr int LOADS = 4 * WGS, MMAS = 4 * WGS + 1, THREADS = 32 * (4 * WGS + 2);   // warps: softmax, loads, MMAs
+  static_assert(COL_END <= TMEM_COLS && TMEM_COLS * CTAS <= 512, "TMEM columns");
+  static_assert(COLS % 16 == 0 && Y_B % (8 * Tile::ROWB) == 0 && X_B % 1024 == 0 && R_B % 64 == 0, "tiles hold whole swizzle atoms");
+  static_assert(BYTES + 1024 <= 227 * 1024, "shared memory");
 };
 
 // MOD: 0 plain scores, 1 capped, 2 with a distance bias (and capped if p.cap > 0).
 template <int D, bool KV, int MOD>
-__global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
+__global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_x2,
                     const __grid_constant__ CUtensorMap tm_y1, const __grid_constant__ CUtensorMap tm_y2,
                     const AttnBwdParams bp) {
-  using Cfg = BwdCfg<D>;
+  using Cfg = BwdCfg<D, KV>;
   using Tile = RowTile<D>;
-  constexpr int T = Cfg::T, NST = Cfg::NST, CH = Cfg::CH;
+  constexpr int T = Cfg::T, NST = Cfg::NST, CH = Cfg::CH, TR = BwdCfg<D, true>::T;   // TR: rows of a block of statistics
   const AttnParams& p = bp.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -96,7 +106,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
   uint64_t* all_done = p_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Cfg::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(sm + Cfg::OFF_MISC + 4);
-  volatile int* range = reinterpret_cast<volatile int*>(sm + Cfg::OFF_MISC + 8);       // [2]
+  volatile int* range = reinterpret_cast<volatile int*>(sm + Cfg::OFF_MISC + 8);       // [4]
   volatile int* last_load = reinterpret_cast<volatile int*>(sm + Cfg::OFF_MISC + 32);  // [NST]
 
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -109,30 +119,35 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
   const int b = bh / heads, hx = bh % heads;
   const BatchMask mask = batch_mask(p.mask, b);
 
-  if (threadIdx.x < 2) {
+  // Stream tiles [range0, range1) that take part, and of the stream's rows those
+  // [range2, range3) that every row of this tile that takes part sees (dQ
+  // pass), or that see all of its keys.
+  if (threadIdx.x < 4) {
+    const int what = threadIdx.x;
     int v = 0;
-    if (KV) {   // rows that see keys [x0, x0 + 128): hi > x0 from the first on, lo < x0 + 128 up to the last
+    if (KV) {   // hi > x0 from the first row on, lo < x0 + 128 up to the last; hi >= x0 + 128, lo <= x0
       int lo = 0, hi = mask.qlen;
       while (lo < hi) {
         const int mid = lo + (hi - lo) / 2;
         const int2 iv = row_interval(mask, mid);
-        if (threadIdx.x == 0 ? iv.y > x0 : iv.x >= x0 + 128) hi = mid; else lo = mid + 1;
+        const bool behind = what == 0 ? iv.y > x0 : what == 1 ? iv.x >= x0 + 128 : what == 2 ? iv.y >= x0 + 128 : iv.x > x0;
+        if (behind) hi = mid; else lo = mid + 1;
       }
-      v = threadIdx.x == 0 ? lo / T : (lo + T - 1) / T;
+      v = what == 0 ? lo / T : what == 1 ? (lo + T - 1) / T : lo;
     } else {
       const int r1 = min(x0 + 128, mask.qlen);
       if (x0 < r1) {
-        const int lo = row_interval(mask, x0).x, hi = row_interval(mask, r1 - 1).y;
-        if (lo < hi) v = threadIdx.x == 0 ? lo / T : (hi + T - 1) / T;
+        const int2 a = row_interval(mask, x0), z = row_interval(mask, r1 - 1);
+        if (a.x < z.y) v = what == 0 ? a.x / T : what == 1 ? (z.y + T - 1) / T : what == 2 ? z.x : a.y;
       }
     }
-    range[threadIdx.x] = v;
+    range[what] = v;
   }
   if (threadIdx.x == 64) {
-    mbar_init(x_full, 1);
+    mbar_init(x_full, Cfg::XT ? 4 * Cfg::WGS : 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 4);
+      mbar_init(p_full + i, Cfg::SHARE ? 4 * Cfg::WGS : 4);
     }
     for (int i = 0; i < NST; ++i) {
       mbar_init(y_full + i, 1);
@@ -143,7 +158,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == Cfg::MMAS) {
     tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
     tmem_relinquish();
   }
@@ -152,21 +167,24 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{p.err, abort_flag, p.timeout_ns};
-  const int t_lo = range[0], per_head = max(0, range[1] - range[0]);
+  const int t_lo = range[0], per_head = max(0, range[1] - range[0]), whole0 = range[2], whole1 = range[3];
   const int N = KV ? per_head * p.G : per_head;   // stream tiles
 
-  if (warp >= 8) {
-    if constexpr (Cfg::WIDE) setmaxnreg_dec<Cfg::LESS>();
-    if (warp == 8) {
+  if (warp >= Cfg::LOADS) {
+    if (warp == Cfg::LOADS) {
       // ------------------------------------------------------------ loads
       if (lane == 0 && N > 0) {
-        tma_prefetch_desc(&tm_x1);
-        tma_prefetch_desc(&tm_x2);
+        if (!Cfg::XT) {
+          tma_prefetch_desc(&tm_x1);
+          tma_prefetch_desc(&tm_x2);
+        }
         tma_prefetch_desc(&tm_y1);
         tma_prefetch_desc(&tm_y2);
-        mbar_arrive_expect_tx(x_full, 2 * Cfg::X_B);
-        Tile::load(sx, &tm_x1, x_full, x0, hx, b, 128);
-        Tile::load(sx + Cfg::X_B, &tm_x2, x_full, x0, hx, b, 128);
+        if (!Cfg::XT) {
+          mbar_arrive_expect_tx(x_full, 2 * Cfg::X_B);
+          Tile::load(sx, &tm_x1, x_full, x0, hx, b, 128);
+          Tile::load(sx + Cfg::X_B, &tm_x2, x_full, x0, hx, b, 128);
+        }
         for (int n = 0; n < N; ++n) {
           const int st = n % NST;
           if (n >= NST && !mbar_wait(y_empty + st, (n / NST - 1) & 1, wc)) break;
@@ -181,7 +199,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
           last_load[st] = n;
         }
       }
-    } else if (warp == 9) {
+    } else {
       // ------------------------------------------------------------ MMAs
       if (N > 0) {   // the whole warp, converged
         const uint32_t idesc_s = idesc_bf16_f32(128, T, false, false);
@@ -189,6 +207,8 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
         const uint64_t x1 = Tile::desc_k(sx), x2 = Tile::desc_k(sx + Cfg::X_B);
         const uint64_t y_k = Tile::desc_k(sy), y_mn = Tile::desc_mn(sy, T);
         constexpr uint64_t TILE = Cfg::Y_B >> 4;
+        // columns of a k-step of 16 weights: each warpgroup packs its own into the first half of its columns
+        auto a_col = [](int ks) { return 16 * ks / Cfg::COLS * Cfg::COLS + 16 * ks % Cfg::COLS / 2; };
         auto issue_scores = [&](int n) -> bool {
           const int st = n % NST;
           if (!mbar_wait_warp(y_full + st, (n / NST) & 1, wc)) return false;
@@ -196,12 +216,16 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
           const uint32_t col = tmem + Cfg::COL_S + (n & 1) * 2 * T;
           const uint64_t y1 = y_k + 2 * st * TILE, y2 = y1 + TILE;
           if (elect_one()) {
-  #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              umma_ss(col, x1 + Tile::kstep_k(kk, 128), y1 + Tile::kstep_k(kk, T), idesc_s, kk > 0 ? 1u : 0u);
-  #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              umma_ss(col + T, x2 + Tile::kstep_k(kk, 128), y2 + Tile::kstep_k(kk, T), idesc_s, kk > 0 ? 1u : 0u);
+#pragma unroll
+            for (int side = 0; side < 2; ++side)
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t y = (side ? y2 : y1) + Tile::kstep_k(kk, T);
+                if constexpr (Cfg::XT)
+                  umma_ts(col + side * T, tmem + (side ? Cfg::COL_X2 : Cfg::COL_X1) + 8 * kk, y, idesc_s, kk > 0 ? 1u : 0u);
+                else
+                  umma_ss(col + side * T, (side ? x2 : x1) + Tile::kstep_k(kk, 128), y, idesc_s, kk > 0 ? 1u : 0u);
+              }
             umma_commit(s_full + (n & 1));
           }
           __syncwarp();
@@ -216,15 +240,15 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
           const uint32_t col = tmem + Cfg::COL_S + (n & 1) * 2 * T;
           const uint64_t y1 = y_mn + 2 * st * TILE, y2 = y1 + TILE;
           if (elect_one()) {
-  #pragma unroll
+#pragma unroll
             for (int ks = 0; ks < T / 16; ++ks)
-              umma_ts(tmem + Cfg::COL_OUT1, col + T + ks * 8, y1 + ks * Tile::KSTEP_MN, idesc_o, (n > 0 || ks > 0) ? 1u : 0u);
-  #pragma unroll
+              umma_ts(tmem + Cfg::COL_OUT1, col + T + a_col(ks), y1 + ks * Tile::KSTEP_MN, idesc_o, (n > 0 || ks > 0) ? 1u : 0u);
+#pragma unroll
             for (int ks = 0; ks < T / 16; ++ks) {
               if (KV)
-                umma_ts(tmem + Cfg::COL_OUT2, col + ks * 8, y2 + ks * Tile::KSTEP_MN, idesc_o, (n > 0 || ks > 0) ? 1u : 0u);
+                umma_ts(tmem + Cfg::COL_OUT2, col + a_col(ks), y2 + ks * Tile::KSTEP_MN, idesc_o, (n > 0 || ks > 0) ? 1u : 0u);
               else   // the low parts of dS
-                umma_ts(tmem + Cfg::COL_OUT1, col + ks * 8, y1 + ks * Tile::KSTEP_MN, idesc_o, 1u);
+                umma_ts(tmem + Cfg::COL_OUT1, col + a_col(ks), y1 + ks * Tile::KSTEP_MN, idesc_o, 1u);
             }
             umma_commit(y_empty + st);
           }
@@ -238,57 +262,80 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
       }
     }
   } else {
-    if constexpr (Cfg::WIDE) setmaxnreg_inc<Cfg::MORE>();
     // ------------------------------------------------------------ softmax
     const int w = warp >> 2, wq = warp & 3;
     const int tid = threadIdx.x & 127;
     const int row = x0 + tid;                       // query (dQ pass) or key of this lane
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-    const uint32_t col_s = lane_base + Cfg::COL_S + w * 2 * T, col_g = col_s + T;
+    constexpr int COLS = Cfg::COLS;
+    const int c0 = Cfg::SHARE ? w * COLS : 0;      // this warpgroup's columns of a tile
     const ScoreOps ops(p.scale, p.cap, false);
     const bool capped = MOD == 1 || (MOD == 2 && p.cap > 0.f);
     // dQ pass: this row's statistics
     float nl2 = -INFINITY, ndelta = 0.f, slope2 = 0.f;
     int lo = 0, hi = 0, pos = 0;
-    float* stat = bp.rows + ((static_cast<long>(b) * p.Hq + hx) * bp.row_blocks + row / T) * (kAttnRowFields * T) + row % T;
+    float* stat = bp.rows + ((static_cast<long>(b) * p.Hq + hx) * bp.row_blocks + row / TR) * (kAttnRowFields * TR) + row % TR;
     if (!KV) {
       if (row < p.mask.Nq) {
         nl2 = stat[0];
-        ndelta = stat[T];
-        lo = __float_as_int(stat[2 * T]);
-        hi = __float_as_int(stat[3 * T]);
-        pos = __float_as_int(stat[4 * T]);
+        ndelta = stat[TR];
+        lo = __float_as_int(stat[2 * TR]);
+        hi = __float_as_int(stat[3 * TR]);
+        pos = __float_as_int(stat[4 * TR]);
       }
       if (MOD == 2) slope2 = p.slopes[hx] * kLog2e;
     }
     uint64_t delta2 = f2_dup(0.f), total2 = delta2;  // dQ pass: sums of P g and of P
     bool ok = true;
-    for (int n = w; n < N; n += 2) {
-      const int st = n % NST;
+    if (Cfg::XT && N > 0) {   // this lane's row of X1 (the first half of the warpgroups) or X2 into TMEM
+      constexpr int EACH = 2 * D / Cfg::WGS;          // elements a warpgroup brings
+      const bool first = w < Cfg::WGS / 2;
+      const int d0 = w % (Cfg::WGS / 2) * EACH;
+      const AttnSide& src = KV ? (first ? bp.k : bp.v) : (first ? bp.q : bp.dy);
+      const uint16_t* xr = src.p + b * src.sb + hx * src.sh + static_cast<long>(row) * src.sn + d0;
+      const bool have = row < (KV ? p.mask.Nk : p.mask.Nq);
+#pragma unroll
+      for (int d = 0; d < EACH; d += 32) {
+        uint32_t r[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = have ? *reinterpret_cast<const uint4*>(xr + d + 8 * i) : make_uint4(0, 0, 0, 0);
+          r[4 * i] = v.x;
+          r[4 * i + 1] = v.y;
+          r[4 * i + 2] = v.z;
+          r[4 * i + 3] = v.w;
+        }
+        tmem_st16(lane_base + (first ? Cfg::COL_X1 : Cfg::COL_X2) + (d0 + d) / 2, r);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive_warp(x_full);
+    }
+    for (int n = Cfg::SHARE ? 0 : w; n < N; n += Cfg::SHARE ? 1 : 2) {
+      const int st = n % NST, buf = n & 1;
+      const uint32_t col_s = lane_base + Cfg::COL_S + buf * 2 * T + c0, col_g = col_s + T;
       const int g = KV ? n / per_head : 0, y0 = (t_lo + n - g * per_head) * T;
       if (KV && MOD == 2) slope2 = p.slopes[hx * p.G + g] * kLog2e;
-      bool dead = false;                            // the streamed row this thread answers for takes no part
-      if (!KV && tid < T && y0 + tid < mask.nk) {
-        dead = y0 + tid >= mask.len;
-        if (mask.doc) {
-          const int2 d = mask.doc[y0 + tid];
-          dead |= d.x == d.y;
-        }
-      }
       const float* rs = reinterpret_cast<const float*>(sr + st * Cfg::R_B);
       const int* ri = reinterpret_cast<const int*>(rs);
-      bool full;
-      if (KV) {
-        // the statistics come with the tile; waiting for it makes them visible to this thread
-        if (!mbar_wait_warp(y_full + st, (n / NST) & 1, wc)) { ok = false; break; }
-        full = y0 + T <= mask.qlen && ri[3 * T] >= x0 + 128 && ri[3 * T - 1] <= x0;
-        dead = tid < T && rs[tid] == -INFINITY;
-      } else {
-        full = __all_sync(~0u, lo <= y0 && hi >= y0 + T);
+      // the statistics come with the tile; waiting for it makes them visible to this thread
+      if (KV && !mbar_wait_warp(y_full + st, (n / NST) & 1, wc)) { ok = false; break; }
+      const bool full = y0 >= whole0 && y0 + T <= whole1;
+      bool dead = false;                            // the streamed row this thread answers for takes no part
+      if (!full && tid < T && (!Cfg::SHARE || w == 0)) {
+        if (KV) {
+          dead = rs[tid] == -INFINITY;
+        } else if (y0 + tid < mask.nk) {
+          dead = y0 + tid >= mask.len;
+          if (mask.doc) {
+            const int2 d = mask.doc[y0 + tid];
+            dead |= d.x == d.y;
+          }
+        }
       }
       // dQ pass, bias: side 1 (-1) where every row of the warp stands behind (before) all keys of the tile
       const int side = KV || MOD != 2 ? 0 : __all_sync(~0u, pos >= y0 + T - 1) ? 1 : __all_sync(~0u, pos <= y0) ? -1 : 0;
-      if (!mbar_wait_warp(s_full + w, (n >> 1) & 1, wc)) { ok = false; break; }
+      if (!mbar_wait_warp(s_full + buf, (n >> 1) & 1, wc)) { ok = false; break; }
       tc_fence_after();
       // one body for tiles that every row sees whole, one for the others
       auto tile = [&](auto whole) {
@@ -299,11 +346,11 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
         tmem_wait_ld();
         regs_loaded(s[0]);
         regs_loaded(gg[0]);
-  #pragma unroll
-        for (int c = 0; c < T; c += CH) {
+#pragma unroll
+        for (int c = 0; c < COLS; c += CH) {
           constexpr int NB = CH;
           const int cur = (c / CH) & 1;
-          if (c + CH < T) {   // the next columns' read in flight
+          if (c + CH < COLS) {   // the next columns' read in flight
             tmem_ld_cols<NB>(col_s + c + CH, s[cur ^ 1]);
             tmem_ld_cols<NB>(col_g + c + CH, gg[cur ^ 1]);
           }
@@ -312,35 +359,35 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
                              __all_sync(~0u, ops.small(fmaxf(max_of(s[cur]), -min_of(s[cur]))));
           // x - l2 of the columns, and 1 - tanh^2
           uint64_t x[CH / 2], dx[CH / 2];
-  #pragma unroll
+#pragma unroll
           for (int q = 0; q < CH / 2; ++q) x[q] = f2(s[cur][2 * q], s[cur][2 * q + 1]);
           if (MOD == 1 || (MOD == 2 && capped)) {
             if (small) {
-  #pragma unroll
+#pragma unroll
               for (int q = 0; q < CH / 2; ++q) x[q] = ops.poly(x[q], f2_dup(0.f));
             } else {
-  #pragma unroll
+#pragma unroll
               for (int q = 0; q < CH / 2; ++q)
                 x[q] = f2_pack(ops.tanh_any(as_f(s[cur][2 * q])), ops.tanh_any(as_f(s[cur][2 * q + 1])));
             }
-  #pragma unroll
+#pragma unroll
             for (int q = 0; q < CH / 2; ++q) dx[q] = f2_fma(f2_mul(x[q], f2_dup(-1.f)), x[q], f2_dup(1.f));
           }
           const uint64_t f = f2_dup(capped ? ops.out : ops.c2);
           uint64_t b2 = f2_dup(0.f), step = b2;
           if (MOD == 2 && !KV && side != 0) step = f2_dup(side > 0 ? 2.f * slope2 : -2.f * slope2);
-  #pragma unroll
+#pragma unroll
           for (int q = 0; q < CH / 2; q += 2) {
             float4 l4 = make_float4(nl2, nl2, nl2, nl2), d4 = make_float4(ndelta, ndelta, ndelta, ndelta);
             if (KV) {
-              l4 = *reinterpret_cast<const float4*>(rs + c + 2 * q);
-              d4 = *reinterpret_cast<const float4*>(rs + T + c + 2 * q);
+              l4 = *reinterpret_cast<const float4*>(rs + c0 + c + 2 * q);
+              d4 = *reinterpret_cast<const float4*>(rs + T + c0 + c + 2 * q);
             }
             const uint64_t ll[2] = {f2_pack(l4.x, l4.y), f2_pack(l4.z, l4.w)};
             const uint64_t dd[2] = {f2_pack(d4.x, d4.y), f2_pack(d4.z, d4.w)};
-  #pragma unroll
+#pragma unroll
             for (int u = 0; u < 2; ++u) {
-              const int k = c + 2 * (q + u);           // the pair's first column
+              const int k = c0 + c + 2 * (q + u);      // the pair's first column
               uint64_t t = f2_fma(x[q + u], f, ll[u]);
               if (MOD == 2) {
                 if (KV) {
@@ -393,7 +440,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
           }
           tmem_st_cols<CH / 2>(col_s + c / 2, KV ? pk : dl);
           tmem_st_cols<CH / 2>(col_g + c / 2, dk);
-          if (c + CH < T) {
+          if (c + CH < COLS) {
             tmem_wait_ld();
             regs_loaded(s[cur ^ 1]);
             regs_loaded(gg[cur ^ 1]);
@@ -411,31 +458,38 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
       __syncwarp();
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive_warp(p_full + w);
+      mbar_arrive_warp(p_full + buf);
     }
     float inv_total = 1.f;
-    if (!KV) {   // both warpgroups' shares; delta and l2 as they come out, for the dK/dV pass
+    if (!KV) {   // the warpgroups' shares; delta and l2 as they come out, for the dK/dV pass
       float d0, d1, t0, t1;
       f2_unpack(delta2, d0, d1);
       f2_unpack(total2, t0, t1);
       float2* share = reinterpret_cast<float2*>(sr);
       share[w * 128 + tid] = make_float2(d0 + d1, t0 + t1);
-      named_bar_sync(1, 256);
-      const float2 a = share[tid], c = share[128 + tid];
-      const float total = a.y + c.y;
+      named_bar_sync(1, 128 * Cfg::WGS);
+      float2 a = share[tid];
+#pragma unroll
+      for (int i = 1; i < Cfg::WGS; ++i) {
+        const float2 c = share[128 * i + tid];
+        a.x += c.x;
+        a.y += c.y;
+      }
+      const float total = a.y;
       inv_total = total > 0.f ? 1.f / total : total;   // NaN stays
       if (w == 0 && row < p.mask.Nq && nl2 != -INFINITY) {
         stat[0] = nl2 - log2f(total);
-        stat[T] = -(a.x + c.x) * inv_total;
+        stat[TR] = -a.x * inv_total;
       }
     }
     if (ok && N > 0) ok = mbar_wait_warp(all_done, 0, wc);
     ok = __all_sync(~0u, ok);
     if (ok) {
       tc_fence_after();
-      // dK/dV pass: warpgroup 0 writes dK, 1 writes dV.  dQ pass: half the columns each (D = 16: all by 0).
-      const bool second = KV && w == 1;
-      const int d_beg = KV || D == 16 ? 0 : w * (D / 2), d_end = KV ? D : D == 16 ? (w == 0 ? D : 0) : d_beg + D / 2;
+      // the outputs' columns are dealt to the warpgroups, 16 at least each: dK then dV, or dQ
+      constexpr int OUT = Cfg::OUTS * D, EACH = OUT / Cfg::WGS < 16 ? 16 : OUT / Cfg::WGS;
+      const bool second = w * EACH >= D;
+      const int d_beg = w * EACH - (second ? D : 0), d_end = w * EACH < OUT ? d_beg + EACH : d_beg;
       const uint32_t col = lane_base + (second ? Cfg::COL_OUT2 : Cfg::COL_OUT1);
       uint16_t* out = second ? bp.dv + b * bp.dvs[0] + hx * bp.dvs[1] + static_cast<long>(row) * bp.dvs[2]
                       : KV   ? bp.dk + b * bp.dks[0] + hx * bp.dks[1] + static_cast<long>(row) * bp.dks[2]
@@ -466,12 +520,12 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, BwdCfg<D>::CTAS)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8 && lane == 0 && N > 0) {   // copies still in flight (only after an abort) must land before exit
+  if (warp == Cfg::LOADS && lane == 0 && N > 0) {   // copies still in flight (only after an abort) must land before exit
     for (int st = 0; st < NST; ++st)
       if (last_load[st] >= 0) mbar_wait_drain(y_full + st, (last_load[st] / NST) & 1, p.timeout_ns);
-    mbar_wait_drain(x_full, 0, p.timeout_ns);
+    if (!Cfg::XT) mbar_wait_drain(x_full, 0, p.timeout_ns);
   }
-  if (warp == 9) {
+  if (warp == Cfg::MMAS) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::TMEM_COLS);
   }
@@ -493,7 +547,7 @@ cudaError_t launch_attn_bwd_pass(const CUtensorMap& x1, const CUtensorMap& x2, c
   };
   auto by_mod = [&](auto d) {
     constexpr int D = decltype(d)::value;
-    using C = BwdCfg<D>;
+    using C = BwdCfg<D, KV>;
     return p.a.slopes      ? go(attn_bwd_kernel<D, KV, 2>, C::BYTES, C::THREADS, C::CTAS)
            : p.a.cap > 0.f ? go(attn_bwd_kernel<D, KV, 1>, C::BYTES, C::THREADS, C::CTAS)
                            : go(attn_bwd_kernel<D, KV, 0>, C::BYTES, C::THREADS, C::CTAS);

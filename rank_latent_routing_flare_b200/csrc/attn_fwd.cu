@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
           const uint64_t qd = q_desc + static_cast<uint64_t>((w * Cfg::Q_B) >> 4);
           const uint64_t kd = k_desc + static_cast<uint64_t>((st * Cfg::KV_B) >> 4);
           if (elect_one()) {
-  #pragma unroll
+#pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               umma_ss(tmem + Cfg::COL_S + w * KT, qd + Tile::kstep_k(kk, QT), kd + Tile::kstep_k(kk, KT), idesc_s,
                       kk > 0 ? 1u : 0u);
@@ -303,19 +303,19 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
         };
         bool ok = mbar_wait_warp(q_full, 0, wc) && mbar_wait_warp(q_full + 1, 0, wc);
         int used[2] = {0, 0};
-  #pragma unroll
+#pragma unroll
         for (int w = 0; w < 2; ++w)
           if (ok && a[w] < e[w] && a[w] == jlo) ok = issue_s(w, 0);
         for (int n = 0; ok && n < ntiles; ++n) {
           const int j = jlo + n, st = n % NST;
-  #pragma unroll
+#pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (ok && j >= a[w] && j < e[w]) {
               ok = mbar_wait_warp(p_full + w, used[w]++ & 1, wc);
               tc_fence_after();
               const uint64_t vd = v_desc + static_cast<uint64_t>((st * Cfg::KV_B) >> 4);
               if (ok && elect_one()) {
-  #pragma unroll
+#pragma unroll
                 for (int ks = 0; ks < KT / 16; ++ks)
                   umma_ts(tmem + Cfg::COL_O + w * D, tmem + Cfg::COL_S + w * KT + ks * 8, vd + ks * Tile::KSTEP_MN,
                           idesc_o, (j > a[w] || ks > 0) ? 1u : 0u);
