@@ -29,9 +29,9 @@
 // keeps dS - bf16(dS) there and adds its product too.  delta from the rounded
 // Y would do the same to dK where a row sees few keys: the dQ pass sums delta
 // = sum_j P_ij g_ij in fp32 on the way and leaves it for the dK/dV pass.  L in
-// fp32 is coarse where the scores are far from 0 (a row far from its keys under
-// a distance bias): the dQ pass also sums P, which should be 1, divides by it
-// and corrects l2 for the other pass.
+// fp32 is coarse for a row far from its keys under a distance bias: there the
+// dQ pass also sums P, which should be 1, divides by it and corrects l2 for the
+// other pass.
 //
 // Streamed rows that take no part (padding) are zeroed in shared memory
 // before the products read them: a weight of 0 does not erase a NaN.
@@ -209,34 +209,35 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
         constexpr uint64_t TILE = Cfg::Y_B >> 4;
         // columns of a k-step of 16 weights: each warpgroup packs its own into the first half of its columns
         auto a_col = [](int ks) { return 16 * ks / Cfg::COLS * Cfg::COLS + 16 * ks % Cfg::COLS / 2; };
-        auto issue_scores = [&](int n) -> bool {
-          const int st = n % NST;
-          if (!mbar_wait_warp(y_full + st, (n / NST) & 1, wc)) return false;
-          tc_fence_after();
+        auto landed = [&](int n) { return n >= N || mbar_wait_warp(y_full + n % NST, (n / NST) & 1, wc); };
+        auto issue_scores = [&](int n) {   // one lane
           const uint32_t col = tmem + Cfg::COL_S + (n & 1) * 2 * T;
-          const uint64_t y1 = y_k + 2 * st * TILE, y2 = y1 + TILE;
-          if (elect_one()) {
+          const uint64_t y1 = y_k + 2 * (n % NST) * TILE, y2 = y1 + TILE;
 #pragma unroll
-            for (int side = 0; side < 2; ++side)
+          for (int side = 0; side < 2; ++side)
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t y = (side ? y2 : y1) + Tile::kstep_k(kk, T);
-                if constexpr (Cfg::XT)
-                  umma_ts(col + side * T, tmem + (side ? Cfg::COL_X2 : Cfg::COL_X1) + 8 * kk, y, idesc_s, kk > 0 ? 1u : 0u);
-                else
-                  umma_ss(col + side * T, (side ? x2 : x1) + Tile::kstep_k(kk, 128), y, idesc_s, kk > 0 ? 1u : 0u);
-              }
-            umma_commit(s_full + (n & 1));
-          }
-          __syncwarp();
-          return true;
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t y = (side ? y2 : y1) + Tile::kstep_k(kk, T);
+              if constexpr (Cfg::XT)
+                umma_ts(col + side * T, tmem + (side ? Cfg::COL_X2 : Cfg::COL_X1) + 8 * kk, y, idesc_s, kk > 0 ? 1u : 0u);
+              else
+                umma_ss(col + side * T, (side ? x2 : x1) + Tile::kstep_k(kk, 128), y, idesc_s, kk > 0 ? 1u : 0u);
+            }
+          umma_commit(s_full + (n & 1));
         };
-        bool ok = mbar_wait_warp(x_full, 0, wc) && issue_scores(0);
-        if (ok && N > 1) ok = issue_scores(1);
+        bool ok = mbar_wait_warp(x_full, 0, wc) && landed(0) && landed(1);
+        tc_fence_after();
+        if (ok && elect_one()) {
+          issue_scores(0);
+          if (N > 1) issue_scores(1);
+        }
+        __syncwarp();
         for (int n = 0; ok && n < N; ++n) {
-          const int st = n % NST;
-          if (!mbar_wait_warp(p_full + (n & 1), (n >> 1) & 1, wc)) break;
+          // the scores of tile n + 2 follow the products of tile n without a gap
+          ok = landed(n + 2) && mbar_wait_warp(p_full + (n & 1), (n >> 1) & 1, wc);
+          if (!ok) break;
           tc_fence_after();
+          const int st = n % NST;
           const uint32_t col = tmem + Cfg::COL_S + (n & 1) * 2 * T;
           const uint64_t y1 = y_mn + 2 * st * TILE, y2 = y1 + TILE;
           if (elect_one()) {
@@ -251,9 +252,9 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
                 umma_ts(tmem + Cfg::COL_OUT1, col + a_col(ks), y1 + ks * Tile::KSTEP_MN, idesc_o, 1u);
             }
             umma_commit(y_empty + st);
+            if (n + 2 < N) issue_scores(n + 2);
           }
           __syncwarp();
-          if (n + 2 < N) ok = issue_scores(n + 2);
         }
         if (elect_one()) umma_commit(all_done);
         __syncwarp();
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
       }
       if (MOD == 2) slope2 = p.slopes[hx] * kLog2e;
     }
-    uint64_t delta2 = f2_dup(0.f), total2 = delta2;  // dQ pass: sums of P g and of P
+    uint64_t delta2 = f2_dup(0.f), total2 = delta2;  // dQ pass: sums of P g and (bias) of P
     bool ok = true;
     if (Cfg::XT && N > 0) {   // this lane's row of X1 (the first half of the warpgroups) or X2 into TMEM
       constexpr int EACH = 2 * D / Cfg::WGS;          // elements a warpgroup brings
@@ -311,10 +312,13 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
       tc_fence_before();
       mbar_arrive_warp(x_full);
     }
-    for (int n = Cfg::SHARE ? 0 : w; n < N; n += Cfg::SHARE ? 1 : 2) {
+    int g = 0, tn = Cfg::SHARE ? 0 : w;               // query head of the key head, tile of that head's stream
+    for (int n = tn; n < N; n += Cfg::SHARE ? 1 : 2, tn += Cfg::SHARE ? 1 : 2) {
+      if (KV)
+        for (; tn >= per_head; tn -= per_head) ++g;
       const int st = n % NST, buf = n & 1;
       const uint32_t col_s = lane_base + Cfg::COL_S + buf * 2 * T + c0, col_g = col_s + T;
-      const int g = KV ? n / per_head : 0, y0 = (t_lo + n - g * per_head) * T;
+      const int y0 = (t_lo + tn) * T;
       if (KV && MOD == 2) slope2 = p.slopes[hx * p.G + g] * kLog2e;
       const float* rs = reinterpret_cast<const float*>(sr + st * Cfg::R_B);
       const int* ri = reinterpret_cast<const int*>(rs);
@@ -432,7 +436,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
                 pk[q + u] = pack_bf16x2(p0, p1);
               } else {
                 delta2 = f2_add(delta2, pg);
-                total2 = f2_add(total2, f2_pack(p0, p1));
+                if (MOD == 2) total2 = f2_add(total2, f2_pack(p0, p1));
                 f2_unpack(f2_fma(f2_pack(bf16_lo(hi16), bf16_hi(hi16)), f2_dup(-1.f), ds), s0, s1);
                 dl[q + u] = pack_bf16x2(s0, s1);
               }
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
         a.x += c.x;
         a.y += c.y;
       }
-      const float total = a.y;
+      const float total = MOD == 2 ? a.y : 1.f;
       inv_total = total > 0.f ? 1.f / total : total;   // NaN stays
       if (w == 0 && row < p.mask.Nq && nl2 != -INFINITY) {
         stat[0] = nl2 - log2f(total);
