@@ -25,14 +25,8 @@ def rows(t):
 def check_rows(name, t, shape, dev, output=False):
     """Checks a bf16 tensor of that shape on GPU `dev`, dense along D, its rows
     on 16-byte boundaries; returns its pointer and strides."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-    if t.dtype is not _bf16:
-        raise TypeError(f"{name} must be {_bf16}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not _bf16 or t.shape != shape:
+        _refuse(name, t, _bf16, shape, dev)
     p, (sb, sh, sn, sd) = t.data_ptr(), t.stride()
     if sd != 1 and shape[3] > 1:
         raise ValueError(f"{name} must be dense along its last dimension")
@@ -48,17 +42,22 @@ def check_small(name, t, dtype, shape, dev) -> int:
     """Checks an optional contiguous tensor on GPU `dev` (shape None: any); returns its pointer."""
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or (
+            shape is not None and t.shape != shape):
+        _refuse(name, t, dtype, shape, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _refuse(name, t, dtype, shape, dev):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def ptr(t) -> int:

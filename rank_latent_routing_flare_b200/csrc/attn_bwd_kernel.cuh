@@ -41,8 +41,10 @@
 #pragma once
 
 #include <type_traits>
+#include <utility>
 
 #include "attn_common.cuh"
+#include "ops_internal.h"
 
 namespace flare {
 
@@ -540,21 +542,22 @@ cudaError_t launch_attn_bwd_pass(const CUtensorMap& x1, const CUtensorMap& x2, c
                                  const CUtensorMap& y2, const AttnBwdParams& p, cudaStream_t s) {
   const long tiles = ((KV ? p.a.mask.Nk : p.a.mask.Nq) + 127) / 128;
   const unsigned grid = static_cast<unsigned>(tiles * p.a.B * (KV ? p.a.Hk : p.a.Hq));
-  auto go = [&](auto kern, int bytes, int threads, int ctas) {
-    // at most `ctas` CTAs share an SM, so that each finds its TMEM columns free
-    const int floor = 228 * 1024 / (ctas + 1) + 1024;
-    const int smem = bytes + 1024 > floor ? bytes + 1024 : floor;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto go = [&](auto d, auto mod) {
+    constexpr int D = decltype(d)::value;
+    using C = BwdCfg<D, KV>;
+    auto* kern = attn_bwd_kernel<D, KV, decltype(mod)::value>;
+    // at most CTAS CTAs share an SM, so that each finds its TMEM columns free
+    constexpr int floor = 228 * 1024 / (C::CTAS + 1) + 1024;
+    constexpr int smem = C::BYTES + 1024 > floor ? C::BYTES + 1024 : floor;
+    const cudaError_t e = allow_smem<std::pair<C, decltype(mod)>>(kern, smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, threads, smem, s>>>(x1, x2, y1, y2, p);
+    kern<<<grid, C::THREADS, smem, s>>>(x1, x2, y1, y2, p);
     return cudaGetLastError();
   };
   auto by_mod = [&](auto d) {
-    constexpr int D = decltype(d)::value;
-    using C = BwdCfg<D, KV>;
-    return p.a.slopes      ? go(attn_bwd_kernel<D, KV, 2>, C::BYTES, C::THREADS, C::CTAS)
-           : p.a.cap > 0.f ? go(attn_bwd_kernel<D, KV, 1>, C::BYTES, C::THREADS, C::CTAS)
-                           : go(attn_bwd_kernel<D, KV, 0>, C::BYTES, C::THREADS, C::CTAS);
+    return p.a.slopes      ? go(d, std::integral_constant<int, 2>{})
+           : p.a.cap > 0.f ? go(d, std::integral_constant<int, 1>{})
+                           : go(d, std::integral_constant<int, 0>{});
   };
   switch (p.a.D) {
     case 16: return by_mod(std::integral_constant<int, 16>{});

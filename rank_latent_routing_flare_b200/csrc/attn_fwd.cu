@@ -33,8 +33,10 @@
 // heads x 4096^2, D = 64: plain 231 us (one CTA: 254), capped 303 (two CTAs,
 // which spill: 364), biased 303 (337); D = 128: plain 291, capped 325.
 #include <climits>
+#include <utility>
 
 #include "attn_common.cuh"
+#include "ops_internal.h"
 
 namespace flare {
 namespace {
@@ -614,7 +616,7 @@ cudaError_t launch_attn_fwd(const AttnMaps& m, const AttnParams& p, cudaStream_t
     // at most CTAS CTAs share an SM, so that each finds its TMEM columns free
     constexpr int floor = 228 * 1024 / (C::CTAS + 1) + 1024;
     constexpr int smem = C::BYTES + 1024 > floor ? C::BYTES + 1024 : floor;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem<std::pair<C, decltype(mod)>>(kern, smem);
     if (e != cudaSuccess) return e;
     kern<<<grid, C::THREADS, smem, s>>>(m.q, m.k, m.v, p);
     return cudaGetLastError();

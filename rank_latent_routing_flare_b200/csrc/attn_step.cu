@@ -14,7 +14,10 @@
 // Rows keep a running reference and sum as in the tiled kernel.  The keys are
 // split over CTAs, within a CTA over 8 warps, which join in shared memory;
 // splits are joined by attn_join.  No lane waits on another CTA.
+#include <type_traits>
+
 #include "attn_common.cuh"
+#include "ops_internal.h"
 
 namespace flare {
 namespace {
@@ -282,19 +285,21 @@ cudaError_t launch_attn_step(const AttnParams& p, const AttnSide& q, const AttnS
   const StepParams sp{p, q, k, v};
   const dim3 grid(static_cast<unsigned>(static_cast<long>(p.splits) * p.B * p.Hk));
   const int rows = p.G * p.mask.Nq, smem = kStepWarps * rows * (p.D + 2) * 4;
-  auto go = [&](auto kern) {
+  auto go = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    auto* kern = attn_step_kernel<D>;
     if (smem > 48 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      const cudaError_t e = allow_smem<StepCfg<D>>(kern, kStepWarps * kAttnStepRows * (D + 2) * 4);
       if (e != cudaSuccess) return e;
     }
     kern<<<grid, kStepWarps * 32, smem, s>>>(sp);
     return cudaGetLastError();
   };
   switch (p.D) {
-    case 16: return go(attn_step_kernel<16>);
-    case 32: return go(attn_step_kernel<32>);
-    case 64: return go(attn_step_kernel<64>);
-    case 128: return go(attn_step_kernel<128>);
+    case 16: return go(std::integral_constant<int, 16>{});
+    case 32: return go(std::integral_constant<int, 32>{});
+    case 64: return go(std::integral_constant<int, 64>{});
+    case 128: return go(std::integral_constant<int, 128>{});
   }
   return cudaErrorInvalidValue;
 }

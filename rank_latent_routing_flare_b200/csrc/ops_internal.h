@@ -1,6 +1,7 @@
 // Argument checks shared by the entry points of include/flare_ops.h.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include "flare_ops.h"
@@ -28,6 +29,22 @@ inline flare_status fill_strides(long (&out)[3], const void* base, const int64_t
     if (s[i] > (int64_t(1) << 38)) return FLARE_ERR_UNSUPPORTED;
   }
   return FLARE_OK;
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory; set once per kernel and
+// device (`Tag` is the kernel's own type), since setting it takes as long as
+// half a launch.
+template <typename Tag, typename Kernel>
+inline cudaError_t allow_smem(Kernel* kern, int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace flare

@@ -26,6 +26,14 @@ def flare_qk_norm_rope_workspace_bytes(B: int, N: int, Hq: int, Hk: int, D: int)
     return int(entry("flare_qk_norm_rope_workspace_bytes")(B, N, Hq, Hk, D))
 
 
+def _check_gain(name, g, H, D, dev):
+    if g is None:
+        return 0
+    if H == 0:
+        raise ValueError(f"{name} is given without its tensor")
+    return check_small(name, g, _f32, (D,) if g.dim() == 1 else (H, D), dev)
+
+
 def _head(Q, K, q_gain, k_gain, freqs, positions, lengths, eps, interleaved, check):
     """The inputs' part of the argument struct, in its order, and (B, N, D, Hq, Hk, device index)."""
     X = Q if Q is not None else K
@@ -49,30 +57,29 @@ def _head(Q, K, q_gain, k_gain, freqs, positions, lengths, eps, interleaved, che
             raise ValueError(f"D is {D}, expected one of {ROW_WIDTHS}")
         q = NO_ROWS if Q is None else check_rows("Q", Q, (B, Hq, N, D), dev)
         k = NO_ROWS if K is None else check_rows("K", K, (B, Hk, N, D), dev)
-        for name, g, h in (("q_gain", q_gain, Hq), ("k_gain", k_gain, Hk)):
-            if g is not None:
-                if h == 0:
-                    raise ValueError(f"{name} is given without its tensor")
-                check_small(name, g, _f32, (D,) if g.dim() == 1 else (h, D), dev)
+        gq = _check_gain("q_gain", q_gain, Hq, D, dev)
+        gk = _check_gain("k_gain", k_gain, Hk, D, dev)
+        fp = check_small("freqs", freqs, _f32, None, dev)
+        n = check_small("lengths", lengths, _i32, (B,), dev)
+        pp = 0
         if freqs is None:
             if positions is not None:
                 raise ValueError("positions are given without freqs")
         else:
             if len(f) not in (1, 2):
                 raise ValueError("freqs is [rot / 2] or [axes, rot / 2]")
-            check_small("freqs", freqs, _f32, None, dev)
             if kind == 1:
-                check_small("positions", positions, _i32, (B, N), dev)
+                pp = check_small("positions", positions, _i32, (B, N), dev)
             elif kind == 2:
-                check_small("positions", positions, _f32, (B, N) if axes == 1 and positions.dim() == 2 else (B, N, axes), dev)
+                pp = check_small("positions", positions, _f32,
+                                 (B, N) if axes == 1 and positions.dim() == 2 else (B, N, axes), dev)
             if kind != 2 and axes != 1:
                 raise ValueError("more than one axis of frequencies needs real coordinates (float32 positions)")
-        check_small("lengths", lengths, _i32, (B,), dev)
     else:
         q, k = (NO_ROWS if t is None else rows(t) for t in (Q, K))
-    packed = (B, N, D, Hq, Hk, rot, axes, bool(interleaved), kind, eps, ptr(freqs), ptr(positions), ptr(lengths), *q, *k,
-              ptr(q_gain), ptr(k_gain), q_gain is not None and q_gain.dim() == 2,
-              k_gain is not None and k_gain.dim() == 2)
+        gq, gk, fp, pp, n = ptr(q_gain), ptr(k_gain), ptr(freqs), ptr(positions), ptr(lengths)
+    packed = (B, N, D, Hq, Hk, rot, axes, bool(interleaved), kind, eps, fp, pp, n, *q, *k, gq, gk,
+              gq != 0 and q_gain.dim() == 2, gk != 0 and k_gain.dim() == 2)
     return packed, (B, N, D, Hq, Hk, dev)
 
 
