@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
 #pragma unroll
             for (int q = 0; q < CH / 2; ++q) dx[q] = f2_fma(f2_mul(x[q], f2_dup(-1.f)), x[q], f2_dup(1.f));
           }
+          const uint32_t bits = FULL || KV ? ~0u : column_bits(lo - y0 - c0, hi - y0 - c0, c);   // columns that the row sees
           const uint64_t f = f2_dup(capped ? ops.out : ops.c2);
           uint64_t b2 = f2_dup(0.f), step = b2;
           if (MOD == 2 && !KV && side != 0) step = f2_dup(side > 0 ? 2.f * slope2 : -2.f * slope2);
@@ -423,8 +424,8 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
                 float a0, a1, b0, b1;
                 f2_unpack(ds, a0, a1);
                 f2_unpack(pg, b0, b1);
-                const bool h0 = KV ? row < ri[2 * T + k] || row >= ri[3 * T + k] : y0 + k < lo || y0 + k >= hi;
-                const bool h1 = KV ? row < ri[2 * T + k + 1] || row >= ri[3 * T + k + 1] : y0 + k + 1 < lo || y0 + k + 1 >= hi;
+                const bool h0 = KV ? row < ri[2 * T + k] || row >= ri[3 * T + k] : !(bits & (1u << (2 * (q + u))));
+                const bool h1 = KV ? row < ri[2 * T + k + 1] || row >= ri[3 * T + k + 1] : !(bits & (2u << (2 * (q + u))));
                 p0 = h0 ? 0.f : p0;
                 p1 = h1 ? 0.f : p1;
                 ds = f2_pack(h0 ? 0.f : a0, h1 ? 0.f : a1);

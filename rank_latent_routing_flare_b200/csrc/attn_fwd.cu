@@ -46,28 +46,30 @@ template <int D, int MOD>
 struct FwdCfg {
   using Tile = RowTile<D>;
   static constexpr bool WIDE = D == 128 || MOD != 0;
+  static constexpr int NQ = 2;                            // query tiles, and softmax warpgroups, of a CTA
   static constexpr int KT = WIDE ? 128 : 64;
   static constexpr int QT = kAttnQTile;
   static constexpr int CTAS = WIDE ? 1 : 2;
   static constexpr int NST = D == 128 ? 2 : D == 64 ? 4 : 6;
   static constexpr int Q_B = Tile::bytes(QT), KV_B = Tile::bytes(KT);
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + 2 * Q_B;
+  static constexpr int OFF_K = OFF_Q + NQ * Q_B;
   static constexpr int OFF_V = OFF_K + NST * KV_B;
   static constexpr int OFF_BAR = OFF_V + NST * KV_B;
   static constexpr int N_BAR = 2 + 2 * NST + 2 + 2 + 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * N_BAR;
   static constexpr int BYTES = OFF_MISC + 32 + 4 * NST;
-  static constexpr uint32_t COL_S = 0, COL_O = 2 * KT;
-  static constexpr uint32_t TMEM_COLS = COL_O + 2 * D <= 256 ? 256 : 512;
-  // Warps 0-3, 4-7: softmax; 8: loads; 9: MMAs.  One CTA an SM: two more fill
-  // a third warpgroup, which gives the softmax threads its registers (168 a
-  // thread at launch).
-  static constexpr int THREADS = WIDE ? 384 : 320;
+  static constexpr uint32_t COL_S = 0, COL_O = NQ * KT;
+  static constexpr uint32_t TMEM_COLS = COL_O + NQ * D <= 256 ? 256 : 512;
+  // Warps: softmax (four per query tile), loads, MMAs.  One CTA an SM:
+  // two more fill a third warpgroup, which gives the softmax threads its
+  // registers (168 a thread at launch).
+  static constexpr int LOADS = 4 * NQ, MMAS = 4 * NQ + 1, THREADS = WIDE ? 384 : 32 * (4 * NQ + 2);
   static constexpr int LESS = 56, MORE = 224;
   static_assert(256 * MORE + 128 * LESS <= 384 * 168, "register split");
-  static_assert(COL_O + 2 * D <= TMEM_COLS && TMEM_COLS * CTAS <= 512, "TMEM columns");
+  static_assert(COL_O + NQ * D <= TMEM_COLS && TMEM_COLS * CTAS <= 512, "TMEM columns");
   static_assert(KV_B % 1024 == 0 && Q_B % 1024 == 0, "tiles hold whole swizzle atoms");
+  static_assert(CTAS * (BYTES + 2048) <= 228 * 1024, "shared memory");
 };
 
 // Key tiles [a, b) that rows [r0, r0 + 128) see.
@@ -88,8 +90,11 @@ __device__ __forceinline__ void unpair(uint64_t v, uint32_t& a, uint32_t& b) {
 template <int N>
 __device__ __forceinline__ void hide(uint32_t (&s)[N], int first, int last) {
 #pragma unroll
-  for (int k = 0; k < N; ++k)
-    if (k < first || k >= last) s[k] = 0xFF800000u;
+  for (int c = 0; c < N; c += 32) {
+    const uint32_t bits = column_bits(first, last, c);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) s[c + k] = bits & (1u << k) ? s[c + k] : 0xFF800000u;
+  }
 }
 // Raw products to capped scores in log2 units, + c.
 template <int N>
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
                     const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
   using Cfg = FwdCfg<D, MOD>;
   using Tile = RowTile<D>;
-  constexpr int KT = Cfg::KT, QT = Cfg::QT, NST = Cfg::NST;
+  constexpr int KT = Cfg::KT, QT = Cfg::QT, NST = Cfg::NST, NQ = Cfg::NQ;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sq = sm + Cfg::OFF_Q;
@@ -203,13 +208,13 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
   // the last query tiles see the most keys under a causal mask: first
   const int qt = n_qt - 1 - static_cast<int>(blockIdx.x) / BH, bh = static_cast<int>(blockIdx.x) % BH;
   const int b = bh / p.Hq, h = bh % p.Hq, hk = h / p.G;
-  const int q0 = qt * 2 * QT, split = blockIdx.y;
+  const int q0 = qt * NQ * QT, split = blockIdx.y;
   const BatchMask mask = batch_mask(p.mask, b);
   pdl_launch_dependents();   // the join of the splits
 
   // The error word is clear before any wait can expire (seconds from now).
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 4) p.err[threadIdx.x] = 0u;
-  if (threadIdx.x < 2) {
+  if (threadIdx.x < NQ) {
     const int2 r = tile_range(mask, q0 + threadIdx.x * QT, KT);
     range[2 * threadIdx.x] = r.x;
     range[2 * threadIdx.x + 1] = r.y;
@@ -230,7 +235,7 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == Cfg::MMAS) {
     tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
     tmem_relinquish();
   }
@@ -241,7 +246,7 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
   const WaitCtx wc{p.err, abort_flag, p.timeout_ns};
 
   // this split's key tiles [jlo, jhi), and of them each query tile's [a, b)
-  int a[2] = {range[0], range[2]}, e[2] = {range[1], range[3]};
+  int a[2] = {range[0], NQ == 2 ? range[2] : 0}, e[2] = {range[1], NQ == 2 ? range[3] : 0};
   int jlo, jhi;
   {
     const bool live0 = a[0] < e[0], live1 = a[1] < e[1];
@@ -259,15 +264,15 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
   }
   const int ntiles = jhi - jlo;
 
-  if (warp >= 8) {
+  if (warp >= Cfg::LOADS) {
     if constexpr (Cfg::WIDE) setmaxnreg_dec<Cfg::LESS>();
-    if (warp == 8) {
+    if (warp == Cfg::LOADS) {
       // ------------------------------------------------------------ loads
       if (lane == 0 && ntiles > 0) {
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
-        for (int w = 0; w < 2; ++w) {
+        for (int w = 0; w < NQ; ++w) {
           mbar_arrive_expect_tx(q_full + w, Cfg::Q_B);   // rows behind the tensor's last come as zeros
           Tile::load(sq + w * Cfg::Q_B, &tm_q, q_full + w, q0 + w * QT, h, b, QT);
         }
@@ -280,7 +285,7 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
           last_load[st] = n;
         }
       }
-    } else if (warp == 9) {
+    } else if (warp == Cfg::MMAS) {
       // ------------------------------------------------------------ MMAs
       if (ntiles > 0) {   // the whole warp, converged
         const uint32_t idesc_s = idesc_bf16_f32(128, KT, false, false);
@@ -303,15 +308,15 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
           __syncwarp();
           return true;
         };
-        bool ok = mbar_wait_warp(q_full, 0, wc) && mbar_wait_warp(q_full + 1, 0, wc);
+        bool ok = mbar_wait_warp(q_full, 0, wc) && (NQ == 1 || mbar_wait_warp(q_full + 1, 0, wc));
         int used[2] = {0, 0};
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
+        for (int w = 0; w < NQ; ++w)
           if (ok && a[w] < e[w] && a[w] == jlo) ok = issue_s(w, 0);
         for (int n = 0; ok && n < ntiles; ++n) {
           const int j = jlo + n, st = n % NST;
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
+          for (int w = 0; w < NQ; ++w) {
             if (ok && j >= a[w] && j < e[w]) {
               ok = mbar_wait_warp(p_full + w, used[w]++ & 1, wc);
               tc_fence_after();
@@ -474,12 +479,12 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8 && lane == 0 && ntiles > 0) {   // copies still in flight (only after an abort) must land before exit
+  if (warp == Cfg::LOADS && lane == 0 && ntiles > 0) {   // copies still in flight (only after an abort) must land before exit
     for (int st = 0; st < NST; ++st)
       if (last_load[st] >= 0) mbar_wait_drain(kv_full + st, (last_load[st] / NST) & 1, p.timeout_ns);
-    for (int w = 0; w < 2; ++w) mbar_wait_drain(q_full + w, 0, p.timeout_ns);
+    for (int w = 0; w < NQ; ++w) mbar_wait_drain(q_full + w, 0, p.timeout_ns);
   }
-  if (warp == 9) {
+  if (warp == Cfg::MMAS) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::TMEM_COLS);
   }
@@ -608,10 +613,10 @@ int attn_fwd_key_tile(int D, bool bias, bool cap) {
 }
 
 cudaError_t launch_attn_fwd(const AttnMaps& m, const AttnParams& p, cudaStream_t s) {
-  const int n_qt = (p.mask.Nq + 2 * kAttnQTile - 1) / (2 * kAttnQTile);
-  const dim3 grid(static_cast<unsigned>(static_cast<long>(n_qt) * p.B * p.Hq), static_cast<unsigned>(p.splits));
   return by_config(p.D, p.slopes != nullptr, p.cap > 0.f, [&](auto d, auto mod, auto c) {
     using C = decltype(c);
+    const long n_qt = (p.mask.Nq + C::NQ * kAttnQTile - 1) / (C::NQ * kAttnQTile);
+    const dim3 grid(static_cast<unsigned>(n_qt * p.B * p.Hq), static_cast<unsigned>(p.splits));
     auto* kern = attn_fwd_kernel<decltype(d)::value, decltype(mod)::value>;
     // at most CTAS CTAs share an SM, so that each finds its TMEM columns free
     constexpr int floor = 228 * 1024 / (C::CTAS + 1) + 1024;

@@ -24,6 +24,12 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   return r;
 }
 
+// Bits [first, last) of the 32 columns from `from` on.
+__device__ __forceinline__ uint32_t column_bits(int first, int last, int from) {
+  const int lo = max(first - from, 0), hi = min(last - from, 32);
+  return lo >= hi ? 0u : (~0u >> (32 - (hi - lo))) << lo;
+}
+
 // Largest of N values (a multiple of 8): four chains.
 template <int N>
 __device__ __forceinline__ float max_of(const uint32_t (&s)[N]) {
