@@ -63,7 +63,7 @@ AttnPlan make_attn_plan(int64_t B, int64_t Hq, int64_t Hk, int64_t Nq, int64_t N
     pl.row_blocks = static_cast<int>(cdiv(Nq, t));
     pl.off_rows = off;
     off += align256(static_cast<size_t>(B * Hq) * pl.row_blocks * t * kAttnRowFields * 4);
-  } else if (pl.splits > 1) {
+  } else if (pl.splits > kAttnClusterSplits) {
     pl.off_part_o = off;
     off += align256(rows * pl.splits * D * 4);
     pl.off_part_l = off;
@@ -193,7 +193,7 @@ flare_status flare_attention_fwd(const flare_attention_args* a, void* workspace,
       return FLARE_ERR_LAUNCH;
     if (launch_attn_fwd(m, p, s) != cudaSuccess) return FLARE_ERR_LAUNCH;
   }
-  if (p.splits > 1 && launch_attn_join(p, s) != cudaSuccess) return FLARE_ERR_LAUNCH;
+  if (p.splits > kAttnClusterSplits && launch_attn_join(p, s) != cudaSuccess) return FLARE_ERR_LAUNCH;
   return FLARE_OK;
 }
 

@@ -23,6 +23,8 @@ struct AttnSide {    // rows [B][H][N][D] with strides in elements
   long sb, sh, sn;
 };
 
+constexpr int kAttnClusterSplits = 8;   // portable cluster size
+
 struct AttnParams {
   int B, Hq, Hk, G, D;           // G = Hq / Hk
   AttnMask mask;
@@ -32,7 +34,8 @@ struct AttnParams {
   uint16_t* y;
   long ys[3];
   float* L;                      // [B][Hq][Nq] or nullptr
-  // work split along the keys: partial results of every split, joined by attn_join
+  // work split along the keys: up to kAttnClusterSplits splits are a cluster
+  // that joins in shared memory; more leave partial results for attn_join
   int splits;
   float* part_o;                 // [splits][B][Hq][Nq][D], each split's normalised output
   float* part_l;                 // [splits][B][Hq][Nq], its log2 sum of weights

@@ -79,6 +79,67 @@ __device__ __forceinline__ void setmaxnreg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Clusters: every thread of every CTA arrives, whatever became of its own waits.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_smem(const void* p, int rank) {   // the same address in another CTA of the cluster
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float peer_load(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_load4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+// Join of a cluster's splits (CTA rank = split): every CTA holds `rows` rows of
+// normalised outputs (STRIDE floats apart) and their log2 sums; each CTA joins
+// its share of the rows and hands them to out(row, first column, four values,
+// log2 sum).  `threads` threads call it, numbered by `t`, between two
+// cluster_sync of all.
+template <int D, int STRIDE, typename Out>
+__device__ __forceinline__ void cluster_join(int splits, int rank, const float* part, const float* lse, int rows, int t,
+                                             int threads, Out&& out) {
+  const int per = (rows + splits - 1) / splits, r0 = rank * per, r1 = min(rows, r0 + per);
+  for (int i = t; i < (r1 - r0) * (D / 4); i += threads) {
+    const int row = r0 + i / (D / 4), d = 4 * (i % (D / 4));
+    float l[kAttnClusterSplits], top = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < kAttnClusterSplits; ++s) {
+      l[s] = s < splits ? peer_load(peer_smem(lse + row, s)) : -INFINITY;
+      top = fmaxf(top, l[s]);
+    }
+    const float base = top == -INFINITY ? 0.f : top;
+    float total = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < kAttnClusterSplits; ++s)
+      if (s < splits) {
+        const float w = ex2_mufu(l[s] - base);
+        const float4 v = peer_load4(peer_smem(part + row * STRIDE + d, s));
+        total += w;
+        a.x = fmaf(w, v.x, a.x);
+        a.y = fmaf(w, v.y, a.y);
+        a.z = fmaf(w, v.z, a.z);
+        a.w = fmaf(w, v.w, a.w);
+      }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    out(row, d, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv), total == 0.f ? -INFINITY : top + log2f(total));
+  }
+}
+// log-sum-exp of a row in natural units, from its log2 sum over biased positions.
+__device__ __forceinline__ float natural_lse(const AttnParams& p, const BatchMask& m, int h, int row, float lse2) {
+  float L = lse2 * 0.69314718055994531f;
+  if (p.slopes && lse2 != -INFINITY) L -= p.slopes[h] * bias_shift(m, row, row_interval(m, row));
+  return L;
+}
+
 // After tcgen05.wait::ld: the registers a TMEM load wrote are defined here,
 // so that no use of them is scheduled before the wait.
 template <int N>

@@ -59,6 +59,9 @@ struct FwdCfg {
   static constexpr int N_BAR = 2 + 2 * NST + 2 + 2 + 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * N_BAR;
   static constexpr int BYTES = OFF_MISC + 32 + 4 * NST;
+  // a cluster's partial outputs, over the operands, and their log2 sums
+  static constexpr int PART = D + 4, OFF_LSE = NQ * QT * PART * 4;
+  static_assert(OFF_LSE + NQ * QT * 4 <= OFF_BAR, "partial results fit over the operands");
   static constexpr uint32_t COL_S = 0, COL_O = NQ * KT;
   static constexpr uint32_t TMEM_COLS = COL_O + NQ * D <= 256 ? 256 : 512;
   // Warps: softmax (four per query tile), loads, MMAs.  One CTA an SM:
@@ -210,7 +213,6 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
   const int b = bh / p.Hq, h = bh % p.Hq, hk = h / p.G;
   const int q0 = qt * NQ * QT, split = blockIdx.y;
   const BatchMask mask = batch_mask(p.mask, b);
-  pdl_launch_dependents();   // the join of the splits
 
   // The error word is clear before any wait can expire (seconds from now).
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 4) p.err[threadIdx.x] = 0u;
@@ -435,18 +437,22 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
       mbar_arrive_warp(p_full + w);
     }
     if (n_w > 0 && ok) ok = mbar_wait_warp(o_full + w, 0, wc);
+    // a cluster's partial results go over the operands: no product may still read those
+    const bool in_cluster = p.splits > 1 && p.splits <= kAttnClusterSplits;
+    if (in_cluster && ntiles > 0) ok = mbar_wait_warp(all_done, 0, wc) && ok;
     ok = __all_sync(~0u, ok);
-    if (ok && q0 + w * QT + wq * 32 < p.mask.Nq) {
+    if (q0 + w * QT + wq * 32 < p.mask.Nq) {
       tc_fence_after();
       const bool have = row < p.mask.Nq;
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const float lse2 = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;   // l: NaN
       const long at = (static_cast<long>(b) * p.Hq + h) * p.mask.Nq + row;
       const long part_row = static_cast<long>(split) * BH * p.mask.Nq + at;
-      if (have) {
+      if (in_cluster) {
+        reinterpret_cast<float*>(sm + Cfg::OFF_LSE)[w * QT + tid] = lse2;
+      } else if (have && ok) {
         if (p.splits > 1) p.part_l[part_row] = lse2;
-        else if (p.L)
-          p.L[at] = lse2 * 0.69314718055994531f - (MOD == 2 && l > 0.f ? p.slopes[h] * bias_shift(mask, row, iv) : 0.f);
+        else if (p.L) p.L[at] = natural_lse(p, mask, h, row, lse2);
       }
       uint16_t* y = p.y + b * p.ys[0] + h * p.ys[1] + static_cast<long>(row) * p.ys[2];
 #pragma unroll
@@ -461,21 +467,35 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
         const bool zero = n_w == 0 || l == 0.f;   // a row that saw no key: whatever O holds
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = zero ? 0.f : __uint_as_float(o[i]) * (l > 0.f ? inv : l);
-        if (have) {
-          if (p.splits > 1) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + part_row * D + d);
+        if (in_cluster || (have && ok && p.splits > 1)) {
+          float4* dst = reinterpret_cast<float4*>(in_cluster ? reinterpret_cast<float*>(sm) + (w * QT + tid) * Cfg::PART + d
+                                                             : p.part_o + part_row * D + d);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(y + d);
+          for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else if (have && ok) {
+          uint4* dst = reinterpret_cast<uint4*>(y + d);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              dst[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                                  pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
-          }
+          for (int i = 0; i < 2; ++i)
+            dst[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
         }
       }
     }
+  }
+  if (p.splits > 1 && p.splits <= kAttnClusterSplits) {
+    __syncwarp();
+    cluster_sync();
+    if (warp < 4 * NQ)
+      cluster_join<D, Cfg::PART>(p.splits, split, reinterpret_cast<float*>(sm), reinterpret_cast<float*>(sm + Cfg::OFF_LSE),
+                                 min(NQ * QT, p.mask.Nq - q0), threadIdx.x, 128 * NQ, [&](int r, int d, float4 v, float lse2) {
+                                   const int row = q0 + r;
+                                   *reinterpret_cast<uint2*>(p.y + b * p.ys[0] + h * p.ys[1] + static_cast<long>(row) * p.ys[2] + d) =
+                                       make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                                   if (d == 0 && p.L)
+                                     p.L[(static_cast<long>(b) * p.Hq + h) * p.mask.Nq + row] = natural_lse(p, mask, h, row, lse2);
+                                 });
+    __syncwarp();
+    cluster_sync();   // the others have read this CTA's rows
   }
   tc_fence_before();
   __syncthreads();
@@ -496,7 +516,6 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
   const long at = static_cast<long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (at >= rows) return;
   const int lane = threadIdx.x & 31;
-  pdl_wait();
   float top = -INFINITY;
   for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_l[s * rows + at]);
   const float base = top == -INFINITY ? 0.f : top;
@@ -517,14 +536,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (lane + 32 * i < p.D) y[lane + 32 * i] = static_cast<uint16_t>(pack_bf16x2(acc[i] * inv, 0.f));
-  if (lane == 0 && p.L) {
-    float L = total == 0.f ? -INFINITY : (top + log2f(total)) * 0.69314718055994531f;
-    if (p.slopes && total > 0.f) {
-      const BatchMask m = batch_mask(p.mask, b);
-      L -= p.slopes[h] * bias_shift(m, n, row_interval(m, n));
-    }
-    p.L[at] = L;
-  }
+  if (lane == 0 && p.L) p.L[at] = natural_lse(p, batch_mask(p.mask, b), h, n, total == 0.f ? -INFINITY : top + log2f(total));
 }
 
 // Documents: the start and the end of the run of equal ids each position lies
@@ -623,15 +635,14 @@ cudaError_t launch_attn_fwd(const AttnMaps& m, const AttnParams& p, cudaStream_t
     constexpr int smem = C::BYTES + 1024 > floor ? C::BYTES + 1024 : floor;
     const cudaError_t e = allow_smem<std::pair<C, decltype(mod)>>(kern, smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, C::THREADS, smem, s>>>(m.q, m.k, m.v, p);
-    return cudaGetLastError();
+    return launch_splits(kern, grid, C::THREADS, smem, s, dim3(1, p.splits, 1), p.splits, m.q, m.k, m.v, p);
   });
 }
 
 cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t s) {
   const long rows = static_cast<long>(p.B) * p.Hq * p.mask.Nq;
-  LaunchCfg lc(dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, true);
-  return cudaLaunchKernelEx(&lc.cfg, attn_join_kernel, p);
+  attn_join_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace flare

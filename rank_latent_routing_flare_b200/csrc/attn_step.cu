@@ -12,8 +12,8 @@
 //    2t+8, 2t+9 and pairs rows with byte permutes; output column n of product i
 //    is element 8n + i.
 // Rows keep a running reference and sum as in the tiled kernel.  The keys are
-// split over CTAs, within a CTA over 8 warps, which join in shared memory;
-// splits are joined by attn_join.  No lane waits on another CTA.
+// split over CTAs, within a CTA over 8 warps, which join in shared memory; up
+// to eight splits are a cluster and join there too.
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -95,7 +95,6 @@ __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_k
   const int split = blockIdx.x % a.splits, bk = blockIdx.x / a.splits, b = bk / a.Hk, hk = bk % a.Hk;
   const int rows = a.G * a.mask.Nq;
   const BatchMask mask = batch_mask(a.mask, b);
-  pdl_launch_dependents();   // the join of the splits
 
   // the keys that any row sees, rounded to chunks and dealt to the splits
   int lo = 0, hi = 0;
@@ -113,6 +112,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_k
   int2 iv[2];
   int pos[2];
   float slope2[2];
+  __shared__ uint4 sm_q[D / 16][32];   // Q's operand fragments, the same for every warp: read per chunk, they hold no registers
   uint32_t qf[D / 16][4];
   const ScoreOps ops(a.scale, a.cap, true);
 #pragma unroll
@@ -134,6 +134,11 @@ __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_k
       }
     }
   }
+  if (warp == 0) {
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) sm_q[k][lane] = make_uint4(qf[k][0], qf[k][1], qf[k][2], qf[k][3]);
+  }
+  __syncthreads();
   const uint16_t* kb = p.k.p + b * p.k.sb + hk * p.k.sh;
   const uint16_t* vb = p.v.p + b * p.v.sb + hk * p.v.sh;
 
@@ -149,15 +154,20 @@ __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_k
   auto compute = [&](const Chunk<D>& c, int key0) {
     float s[2][4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
 #pragma unroll
-      for (int blk = 0; blk < C::KB; ++blk)
+    for (int blk = 0; blk < C::KB; ++blk)
 #pragma unroll
-        for (int u = 0; u < C::KE / 4; ++u)
-          mma16816(s[n], qf[blk * (C::KE / 4) + u], c.k[n][blk][2 * u], c.k[n][blk][2 * u + 1]);
-    }
+      for (int u = 0; u < C::KE / 4; ++u) {
+        uint32_t q[4];
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
+                     : "r"(smem_u32(&sm_q[blk * (C::KE / 4) + u][lane])));
+#pragma unroll
+        for (int n = 0; n < 2; ++n) mma16816(s[n], q, c.k[n][blk][2 * u], c.k[n][blk][2 * u + 1]);
+      }
     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int n = 0; n < 2; ++n)
@@ -223,6 +233,10 @@ __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_k
   // join the warps: row statistics, then the outputs
   float* sm_ml = sh;
   float* sm_o = sh + 2 * kStepWarps * rows;
+  // a cluster's partial outputs and log2 sums, behind the warps'
+  float* sm_part = sm_o + kStepWarps * rows * D;
+  float* sm_lse = sm_part + rows * (D + 4);
+  const bool in_cluster = a.splits > 1 && a.splits <= kAttnClusterSplits;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     l[u] += __shfl_xor_sync(~0u, l[u], 1);
@@ -263,20 +277,33 @@ __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_k
     const long at = (static_cast<long>(b) * a.Hq + h) * a.mask.Nq + i;
     const float inv = total == 0.f ? 0.f : 1.f / total;
     const float lse2 = total == 0.f ? -INFINITY : top + log2f(total);
-    if (a.splits > 1) {
+    if (in_cluster) {
+      *reinterpret_cast<float2*>(sm_part + r * (D + 4) + d) = make_float2(x0 * inv, x1 * inv);
+      if (d == 0) sm_lse[r] = lse2;
+    } else if (a.splits > 1) {
       const long part = static_cast<long>(split) * a.B * a.Hq * a.mask.Nq + at;
       *reinterpret_cast<float2*>(a.part_o + part * D + d) = make_float2(x0 * inv, x1 * inv);
       if (d == 0) a.part_l[part] = lse2;
     } else {
       *reinterpret_cast<uint32_t*>(a.y + b * a.ys[0] + h * a.ys[1] + i * a.ys[2] + d) = pack_bf16x2(x0 * inv, x1 * inv);
-      if (d == 0 && a.L) {
-        float L = lse2 * 0.69314718055994531f;
-        if (a.slopes && total > 0.f) L -= a.slopes[h] * bias_shift(mask, i, row_interval(mask, i));
-        a.L[at] = L;
-      }
+      if (d == 0 && a.L) a.L[at] = natural_lse(a, mask, h, i, lse2);
     }
   }
+  if (in_cluster) {
+    cluster_sync();
+    cluster_join<D, D + 4>(a.splits, split, sm_part, sm_lse, rows, threadIdx.x, blockDim.x, [&](int r, int d, float4 v, float lse2) {
+      const int i = r / a.G, h = hk * a.G + r % a.G;
+      *reinterpret_cast<uint2*>(a.y + b * a.ys[0] + h * a.ys[1] + i * a.ys[2] + d) =
+          make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      if (d == 0 && a.L) a.L[(static_cast<long>(b) * a.Hq + h) * a.mask.Nq + i] = natural_lse(a, mask, h, i, lse2);
+    });
+    __syncwarp();
+    cluster_sync();   // the others have read this CTA's rows
+  }
 }
+
+// Row statistics and outputs of the warps, and of the CTA for its cluster.
+constexpr int step_smem(int rows, int D) { return 4 * rows * (kStepWarps * (D + 2) + D + 5); }
 
 }  // namespace
 
@@ -284,16 +311,15 @@ cudaError_t launch_attn_step(const AttnParams& p, const AttnSide& q, const AttnS
                              cudaStream_t s) {
   const StepParams sp{p, q, k, v};
   const dim3 grid(static_cast<unsigned>(static_cast<long>(p.splits) * p.B * p.Hk));
-  const int rows = p.G * p.mask.Nq, smem = kStepWarps * rows * (p.D + 2) * 4;
+  const int rows = p.G * p.mask.Nq, smem = step_smem(rows, p.D);
   auto go = [&](auto d) {
     constexpr int D = decltype(d)::value;
     auto* kern = attn_step_kernel<D>;
     if (smem > 48 * 1024) {
-      const cudaError_t e = allow_smem<StepCfg<D>>(kern, kStepWarps * kAttnStepRows * (D + 2) * 4);
+      const cudaError_t e = allow_smem<StepCfg<D>>(kern, step_smem(kAttnStepRows, D));
       if (e != cudaSuccess) return e;
     }
-    kern<<<grid, kStepWarps * 32, smem, s>>>(sp);
-    return cudaGetLastError();
+    return launch_splits(kern, grid, kStepWarps * 32, smem, s, dim3(p.splits, 1, 1), p.splits, sp);
   };
   switch (p.D) {
     case 16: return go(std::integral_constant<int, 16>{});

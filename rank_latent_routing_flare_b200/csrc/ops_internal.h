@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cstdint>
 
+#include "attention.h"
 #include "flare_ops.h"
 #include "host_internal.h"
 
@@ -45,6 +46,26 @@ inline cudaError_t allow_smem(Kernel* kern, int bytes) {
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
+}
+
+// Launch of a kernel whose splits along the keys are a cluster (where there
+// are few enough), or are joined by a kernel behind it.
+template <typename Kernel, typename... Args>
+inline cudaError_t launch_splits(Kernel* kern, dim3 grid, int threads, size_t smem, cudaStream_t s, dim3 cluster, int splits,
+                                 const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster.x;
+  attr.val.clusterDim.y = cluster.y;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = splits > 1 && splits <= kAttnClusterSplits ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 }  // namespace flare
