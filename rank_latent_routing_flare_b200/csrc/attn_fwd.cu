@@ -247,7 +247,10 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{p.err, abort_flag, p.timeout_ns};
 
-  // this split's key tiles [jlo, jhi), and of them each query tile's [a, b)
+  // this split's key tiles [jlo, jhi), taken in steps n = 0, 1, ...: from the
+  // last one down under a distance bias, whose rows then meet their nearest
+  // keys early and raise their reference no more (a causal mask puts those
+  // last).  Each query tile takes part in steps [a, e).
   int a[2] = {range[0], NQ == 2 ? range[2] : 0}, e[2] = {range[1], NQ == 2 ? range[3] : 0};
   int jlo, jhi;
   {
@@ -259,12 +262,14 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
     jhi = min(jhi, jlo + per);
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      a[w] = max(a[w], jlo);
-      e[w] = min(e[w], jhi);
+      const int first = max(a[w], jlo), end = min(e[w], jhi);
+      a[w] = MOD == 2 ? jhi - end : first - jlo;
+      e[w] = MOD == 2 ? jhi - first : end - jlo;
       if (a[w] >= e[w]) a[w] = e[w] = 0;
     }
   }
   const int ntiles = jhi - jlo;
+  auto key0 = [&](int n) { return (MOD == 2 ? jhi - 1 - n : jlo + n) * KT; };   // first key of step n
 
   if (warp >= Cfg::LOADS) {
     if constexpr (Cfg::WIDE) setmaxnreg_dec<Cfg::LESS>();
@@ -282,8 +287,8 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
           const int st = n % NST;
           if (n >= NST && !mbar_wait(kv_empty + st, (n / NST - 1) & 1, wc)) break;
           mbar_arrive_expect_tx(kv_full + st, 2 * Cfg::KV_B);
-          Tile::load(sk + st * Cfg::KV_B, &tm_k, kv_full + st, (jlo + n) * KT, hk, b, KT);
-          Tile::load(sv + st * Cfg::KV_B, &tm_v, kv_full + st, (jlo + n) * KT, hk, b, KT);
+          Tile::load(sk + st * Cfg::KV_B, &tm_k, kv_full + st, key0(n), hk, b, KT);
+          Tile::load(sv + st * Cfg::KV_B, &tm_v, kv_full + st, key0(n), hk, b, KT);
           last_load[st] = n;
         }
       }
@@ -314,12 +319,12 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
         int used[2] = {0, 0};
 #pragma unroll
         for (int w = 0; w < NQ; ++w)
-          if (ok && a[w] < e[w] && a[w] == jlo) ok = issue_s(w, 0);
+          if (ok && a[w] < e[w] && a[w] == 0) ok = issue_s(w, 0);
         for (int n = 0; ok && n < ntiles; ++n) {
-          const int j = jlo + n, st = n % NST;
+          const int st = n % NST;
 #pragma unroll
           for (int w = 0; w < NQ; ++w) {
-            if (ok && j >= a[w] && j < e[w]) {
+            if (ok && n >= a[w] && n < e[w]) {
               ok = mbar_wait_warp(p_full + w, used[w]++ & 1, wc);
               tc_fence_after();
               const uint64_t vd = v_desc + static_cast<uint64_t>((st * Cfg::KV_B) >> 4);
@@ -327,12 +332,12 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
 #pragma unroll
                 for (int ks = 0; ks < KT / 16; ++ks)
                   umma_ts(tmem + Cfg::COL_O + w * D, tmem + Cfg::COL_S + w * KT + ks * 8, vd + ks * Tile::KSTEP_MN,
-                          idesc_o, (j > a[w] || ks > 0) ? 1u : 0u);
-                if (j + 1 == e[w]) umma_commit(o_full + w);
+                          idesc_o, (n > a[w] || ks > 0) ? 1u : 0u);
+                if (n + 1 == e[w]) umma_commit(o_full + w);
               }
               __syncwarp();
             }
-            if (ok && j + 1 >= a[w] && j + 1 < e[w]) ok = issue_s(w, n + 1);
+            if (ok && n + 1 >= a[w] && n + 1 < e[w]) ok = issue_s(w, n + 1);
           }
           if (elect_one()) umma_commit(kv_empty + st);
           __syncwarp();
@@ -360,7 +365,7 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
     bool ok = true;
     const int a_w = w ? a[1] : a[0], n_w = (w ? e[1] : e[0]) - a_w;
     for (int it = 0; it < n_w; ++it) {
-      const int j = a_w + it, k0 = j * KT, n = j - jlo, st = n % NST;
+      const int n = a_w + it, k0 = key0(n), st = n % NST;
       // the V row this thread answers for: a key that no query may see
       bool dead = false;
       if (KT == 128 || tid < KT) {
