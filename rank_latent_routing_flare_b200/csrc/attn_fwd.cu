@@ -158,6 +158,34 @@ __device__ __forceinline__ float weights(const uint32_t (&s)[N], float c2, float
   f2_unpack(f2_add(sum0, sum1), a, b);
   return a + b;
 }
+// As weights<N, true>, with a bias linear in the column (see bias_scores).
+template <int N>
+__device__ __forceinline__ float biased_weights(const uint32_t (&s)[N], float c2, float base, float d, float slope2, int side,
+                                                uint32_t col) {
+  const uint64_t c = f2_dup(c2);
+  const float g = side > 0 ? -slope2 : slope2;
+  const uint64_t step = f2_dup(-2.f * g);
+  uint64_t sum0 = f2_dup(0.f), sum1 = sum0;
+#pragma unroll
+  for (int k = 0; k < N; k += 32) {
+    uint32_t pk[16];
+    uint64_t b;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      if (q % 8 == 0) b = f2_pack(fmaf(g, d - (k + 2 * q), -base), fmaf(g, d - (k + 2 * q + 1), -base));
+      float p0, p1;
+      ex2_pair(f2_fma(f2(s[k + 2 * q], s[k + 2 * q + 1]), c, b), p0, p1);
+      b = f2_add(b, step);
+      if (q & 1) sum1 = f2_add(sum1, f2_pack(p0, p1));
+      else sum0 = f2_add(sum0, f2_pack(p0, p1));
+      pk[q] = pack_bf16x2(p0, p1);
+    }
+    tmem_st16(col + k / 2, pk);
+  }
+  float x, y;
+  f2_unpack(f2_add(sum0, sum1), x, y);
+  return x + y;
+}
 // As weights<N, true>, for capped scores of raw products: tanh and the shift
 // by the base in one polynomial.  Needs small.
 template <int N>
@@ -388,6 +416,8 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
       // and a shift replace the products here
       float mx;
       bool small = false;
+      enum { kExact, kLinear, kNone } how = kExact;   // MOD 2: scores in place, bias to be added, weights all 0
+      int linear_side = 0;
       if (MOD == 0) {
         if (masked) hide<KT>(s, first, last);
         mx = max_of(s) * ops.c2;
@@ -405,11 +435,28 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
       } else {
         if (capped) cap_scores<KT>(s, ops, __all_sync(~0u, ops.small(fmaxf(max_of(s), -min_of(s)))), 0.f);
         const int side = __all_sync(~0u, pos >= k0 + KT - 1) ? 1 : __all_sync(~0u, pos <= k0) ? -1 : 0;
-        bias_scores<KT>(s, capped ? 1.f : ops.c2, static_cast<float>(pos - k0), slope2, side);
-        if (masked) hide<KT>(s, first, last);
-        mx = max_of(s);
+        const float c = capped ? 1.f : ops.c2;
+        // A tile that every row sees, all on one side: no score is above the
+        // largest product with the smallest distance's bias (a negative
+        // slope's largest).  Weights below 2^-64 of the reference change no
+        // fp32 sum: such a tile's are 0 (but a NaN is kept).  Otherwise the bound serves as the
+        // maximum where it is not far above it.
+        if (side != 0 && !masked) {
+          const int near = side > 0 ? pos - (k0 + KT - 1) : k0 - pos;
+          mx = fmaf(max_of<KT, true>(s), c, -slope2 * static_cast<float>(slope2 >= 0.f ? near : near + KT - 1));
+          const bool steep = fabsf(slope2) * (KT - 1) > 64.f;
+          how = it > 0 && __all_sync(~0u, mx < m - 64.f) ? kNone : steep ? kExact : kLinear;
+        }
+        if (how == kExact) {
+          bias_scores<KT>(s, c, static_cast<float>(pos - k0), slope2, side);
+          if (masked) hide<KT>(s, first, last);
+          mx = max_of(s);
+        }
+        linear_side = side;
       }
-      if (it == 0) {
+      if (MOD == 2 && how == kNone) {
+        // the reference stays
+      } else if (it == 0) {
         m = mx;
       } else if (__any_sync(~0u, mx > m + 8.f)) {
         const float m_new = fmaxf(m, mx);
@@ -428,8 +475,18 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
         }
       }
       const float base = m == -INFINITY ? 0.f : m;
-      const float sum = MOD == 1 && small && !masked ? capped_weights<KT>(s, ops, base, col_s)
-                                                     : weights<KT, MOD == 0>(s, ops.c2, base, col_s);
+      float sum = 0.f;
+      if (MOD == 2 && how == kNone) {
+        uint32_t none[16] = {};
+#pragma unroll
+        for (int k = 0; k < KT; k += 32) tmem_st16(col_s + k / 2, none);
+      } else if (MOD == 2 && how == kLinear) {
+        sum = biased_weights<KT>(s, capped ? 1.f : ops.c2, base, static_cast<float>(pos - k0), slope2, linear_side, col_s);
+      } else if (MOD == 1 && small && !masked) {
+        sum = capped_weights<KT>(s, ops, base, col_s);
+      } else {
+        sum = weights<KT, MOD == 0>(s, ops.c2, base, col_s);
+      }
       l += sum;
       if (dead) {
         if (!mbar_wait(kv_full + st, (n / NST) & 1, wc)) ok = false;   // landed before the scores were computed

@@ -10,9 +10,11 @@
 
 namespace flare {
 
+template <bool NAN_TOO>
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  if (NAN_TOO) asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  else asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ float as_f(uint32_t x) { return __uint_as_float(x); }
@@ -30,17 +32,18 @@ __device__ __forceinline__ uint32_t column_bits(int first, int last, int from) {
   return lo >= hi ? 0u : (~0u >> (32 - (hi - lo))) << lo;
 }
 
-// Largest of N values (a multiple of 8): four chains.
-template <int N>
+// Largest of N values (a multiple of 8): four chains.  NAN_TOO: NaN if one is
+// (else NaN is passed over).
+template <int N, bool NAN_TOO = false>
 __device__ __forceinline__ float max_of(const uint32_t (&s)[N]) {
   float a[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) a[c] = fmaxf(as_f(s[2 * c]), as_f(s[2 * c + 1]));
+  for (int c = 0; c < 4; ++c) a[c] = max3<NAN_TOO>(as_f(s[2 * c]), as_f(s[2 * c + 1]), as_f(s[2 * c + 1]));
 #pragma unroll
   for (int k = 8; k < N; k += 8)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) a[c] = max3(a[c], as_f(s[k + 2 * c]), as_f(s[k + 2 * c + 1]));
-  return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+    for (int c = 0; c < 4; ++c) a[c] = max3<NAN_TOO>(a[c], as_f(s[k + 2 * c]), as_f(s[k + 2 * c + 1]));
+  return max3<NAN_TOO>(max3<NAN_TOO>(a[0], a[1], a[2]), a[3], a[3]);
 }
 // Smallest of N values, likewise.
 template <int N>

@@ -151,6 +151,26 @@ def test_large_scores_and_growing_maxima():
         check(Q, K, V, dY, {"scale": 0.01})
 
 
+@pytest.mark.parametrize("D", [32, 128])
+@pytest.mark.parametrize("opts", [{}, {"cap": 20.0}, {"steep": True, "causal": True}, {"steep": True, "cap": 20.0}],
+                         ids=["plain", "cap", "bias", "bias_cap"])
+def test_nan_of_a_visible_key_shows(D, opts):
+    """A NaN in a key or value that a row sees reaches the row, however small its weight would be."""
+    opts = dict(opts)
+    if opts.pop("steep", False):
+        opts["slopes"] = torch.full((2,), 4.0, device=DEV)
+    Q, K, V, _, _ = make(1, 2, 2, 700, 700, D, seed=11)
+    for x in (K, V):
+        old = x[0, 1, 3].clone()
+        x[0, 1, 3] = math.nan
+        Y = fl.flare_attention_fwd(Q, K, V, **opts)
+        first = 3 if opts.get("causal") else 0
+        assert torch.isnan(Y[0, 1, first:]).all() and torch.isfinite(Y[0, 0]).all()
+        step = fl.flare_attention_fwd(Q[:, :, -1:], K, V, **opts)
+        assert torch.isnan(step[0, 1]).all() and torch.isfinite(step[0, 0]).all()
+        x[0, 1, 3] = old
+
+
 def test_strided_outputs_streams_and_graph():
     Q, K, V, dY, o = make(2, 4, 2, 200, 200, 64, seed=4, causal=True, cap=10.0, documents=documents(2, 200, (90,)))
     Y, L = fl.flare_attention_fwd_train(Q, K, V, **o)
