@@ -227,11 +227,18 @@ flare_status flare_attention_bwd(const flare_attention_args* a, void* workspace,
   // the dQ pass keeps tiles of 128 rows of Q and dY and streams K and V; the dK/dV pass the other way round
   const int tq = attn_bwd_stream_tile(p.a.D, false), tkv = attn_bwd_stream_tile(p.a.D, true);
   AttnMaps dq, dkv;
-  if (!map_rows(&dq.q, a->Q, r.q, a->B, a->Hq, a->Nq, a->D, 128) || !map_rows(&dq.dy, a->dY, dys, a->B, a->Hq, a->Nq, a->D, 128) ||
-      !map_rows(&dq.k, a->K, r.k, a->B, a->Hk, a->Nk, a->D, tq) || !map_rows(&dq.v, a->V, r.v, a->B, a->Hk, a->Nk, a->D, tq) ||
-      !map_rows(&dkv.q, a->Q, r.q, a->B, a->Hq, a->Nq, a->D, tkv) || !map_rows(&dkv.dy, a->dY, dys, a->B, a->Hq, a->Nq, a->D, tkv) ||
-      !map_rows(&dkv.k, a->K, r.k, a->B, a->Hk, a->Nk, a->D, 128) || !map_rows(&dkv.v, a->V, r.v, a->B, a->Hk, a->Nk, a->D, 128))
-    return FLARE_ERR_LAUNCH;
+  // a pass that keeps its own tile of rows in TMEM reads it without a map (any map stands in)
+  bool ok = map_rows(&dq.k, a->K, r.k, a->B, a->Hk, a->Nk, a->D, tq) && map_rows(&dq.v, a->V, r.v, a->B, a->Hk, a->Nk, a->D, tq) &&
+            map_rows(&dkv.q, a->Q, r.q, a->B, a->Hq, a->Nq, a->D, tkv) && map_rows(&dkv.dy, a->dY, dys, a->B, a->Hq, a->Nq, a->D, tkv);
+  dq.q = dq.k;
+  dq.dy = dq.v;
+  if (!attn_bwd_rows_in_tmem(p.a.D, false))
+    ok = ok && map_rows(&dq.q, a->Q, r.q, a->B, a->Hq, a->Nq, a->D, 128) && map_rows(&dq.dy, a->dY, dys, a->B, a->Hq, a->Nq, a->D, 128);
+  dkv.k = dkv.q;
+  dkv.v = dkv.dy;
+  if (!attn_bwd_rows_in_tmem(p.a.D, true))
+    ok = ok && map_rows(&dkv.k, a->K, r.k, a->B, a->Hk, a->Nk, a->D, 128) && map_rows(&dkv.v, a->V, r.v, a->B, a->Hk, a->Nk, a->D, 128);
+  if (!ok) return FLARE_ERR_LAUNCH;
   if (launch_attn_bwd_dq(dq, p, s) != cudaSuccess || launch_attn_bwd_dkv(dkv, p, s) != cudaSuccess)
     return FLARE_ERR_LAUNCH;
   return FLARE_OK;

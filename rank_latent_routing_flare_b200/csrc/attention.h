@@ -57,6 +57,7 @@ struct AttnBwdParams {
   long dqs[3], dks[3], dvs[3];
   float* rows;
   int row_blocks;                // blocks per head
+  int split_bits;                // dK/dV pass: log2 of the CTAs that share a key tile's stream
 };
 
 struct AttnMaps {                // tensor maps of the kernels' operands
@@ -76,6 +77,7 @@ cudaError_t launch_attn_step(const AttnParams& p, const AttnSide& q, const AttnS
                              cudaStream_t s);
 
 int attn_bwd_stream_tile(int D, bool kv);   // rows per streamed tile of the dQ pass and of the dK/dV pass
+bool attn_bwd_rows_in_tmem(int D, bool kv);  // whether a pass reads its own tile of rows without a map
 cudaError_t launch_attn_rows(const AttnBwdParams& p, cudaStream_t s);
 cudaError_t launch_attn_bwd_dq(const AttnMaps& m, const AttnBwdParams& p, cudaStream_t s);
 cudaError_t launch_attn_bwd_dkv(const AttnMaps& m, const AttnBwdParams& p, cudaStream_t s);

@@ -54,6 +54,10 @@ int attn_bwd_stream_tile(int D, bool kv) {
                    : (kv ? BwdCfg<32, true>::T : BwdCfg<32, false>::T);
 }
 
+bool attn_bwd_rows_in_tmem(int D, bool kv) {
+  return D == 128 ? (kv ? BwdCfg<128, true>::XT : BwdCfg<128, false>::XT) : D == 64 && (kv ? BwdCfg<64, true>::XT : BwdCfg<64, false>::XT);
+}
+
 cudaError_t launch_attn_rows(const AttnBwdParams& p, cudaStream_t s) {
   auto go = [&](auto d) {
     constexpr int D = decltype(d)::value, ROWS = 256 / (D / 8);

@@ -27,11 +27,16 @@
 // Roundings.  dS in bf16 is off by up to 2^-8 and would make dQ half again as
 // inexact as its own rounding to bf16; the dQ pass, whose S columns are free,
 // keeps dS - bf16(dS) there and adds its product too.  delta from the rounded
-// Y would do the same to dK where a row sees few keys: the dQ pass sums delta
-// = sum_j P_ij g_ij in fp32 on the way and leaves it for the dK/dV pass.  L in
+// Y would do the same where a row sees few keys: the dQ pass sums delta
+// = sum_j P_ij g_ij in fp32 on the way and leaves it for the dK/dV pass, and with
+// few keys it sums in a first sweep over them and has the use of it itself.  L in
 // fp32 is coarse for a row far from its keys under a distance bias: there the
 // dQ pass also sums P, which should be 1, divides by it and corrects l2 for the
 // other pass.
+//
+// Few key heads under many rows leave most SMs without a tile in the dK/dV
+// pass: there up to eight CTAs, a cluster, share a tile's stream and add their
+// partial sums in a fixed order over each other's shared memory.
 //
 // Streamed rows that take no part (padding) are zeroed in shared memory
 // before the products read them: a weight of 0 does not erase a NaN.
@@ -40,6 +45,7 @@
 // columns, two CTAs per SM; the exponentials bound those.
 #pragma once
 
+#include <tuple>
 #include <type_traits>
 #include <utility>
 
@@ -48,14 +54,19 @@
 
 namespace flare {
 
-#ifndef TKV128
-#define TKV128 64
-#endif
+// Up to this many keys the dQ pass sums delta and the weights before it uses
+// them: delta from the rounded Y is off by what one key weighs.  Norm of dQ's
+// error, of its values' rounding to bf16, with one sweep (two): 1.4 (1.0) at 100
+// keys, 1.2 (1.0) at 370, 1.5 (1.0) at 900 under a bias, 1.15 at 2000, 1.1 at
+// 4000.  The first sweep adds 40 to 90 % to this pass, at such sizes 3 to 6 us
+// of a step that takes 50 to 60 on the host; at 4000 keys it would be a quarter of the step.
+constexpr int kAttnTwiceKeys = 1024;
+
 template <int D_, bool KV>
 struct BwdCfg {
   static constexpr int D = D_;
   using Tile = RowTile<D>;
-  static constexpr int T = D <= 32 ? 48 : KV && D == 128 ? TKV128 : 64;
+  static constexpr int T = D <= 32 ? 48 : 64;
   // Wide heads, one CTA an SM: four warpgroups share a tile, a quarter of its
   // columns each.  Narrow ones, two CTAs an SM: two warpgroups take tiles in turn.
   static constexpr bool SHARE = D >= 64;
@@ -82,11 +93,14 @@ struct BwdCfg {
   static constexpr int LOADS = 4 * WGS, MMAS = 4 * WGS + 1, THREADS = 32 * (4 * WGS + 2);   // warps: softmax, loads, MMAs
   static_assert(COL_END <= TMEM_COLS && TMEM_COLS * CTAS <= 512, "TMEM columns");
   static_assert(COLS % 16 == 0 && Y_B % (8 * Tile::ROWB) == 0 && X_B % 1024 == 0 && R_B % 64 == 0, "tiles hold whole swizzle atoms");
+  static constexpr int PART = OUTS * D + 4;               // floats between rows of a split's partial outputs
+  static_assert(!KV || 128 * PART * 4 <= OFF_BAR, "partial outputs go over the operands and the statistics");
   static_assert(BYTES + 1024 <= 227 * 1024, "shared memory");
 };
 
 // MOD: 0 plain scores, 1 capped, 2 with a distance bias (and capped if p.cap > 0).
-template <int D, bool KV, int MOD>
+// TWICE (dQ pass): a first sweep over the keys sums delta and the weights.
+template <int D, bool KV, int MOD, bool TWICE>
 __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_x2,
                     const __grid_constant__ CUtensorMap tm_y1, const __grid_constant__ CUtensorMap tm_y2,
@@ -115,8 +129,10 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
   // the dQ pass owns query heads and begins with the last rows, the dK/dV
   // pass owns key heads and begins with the first keys: under a causal mask
   // those have the most to do
-  const int heads = KV ? p.Hk : p.Hq, n_tiles = gridDim.x / (p.B * heads);
-  const int ti = static_cast<int>(blockIdx.x) / (p.B * heads), bh = static_cast<int>(blockIdx.x) % (p.B * heads);
+  const int split_bits = KV ? bp.split_bits : 0, splits = 1 << split_bits, split = blockIdx.x & (splits - 1);
+  const int block = static_cast<int>(blockIdx.x) >> split_bits, blocks = static_cast<int>(gridDim.x) >> split_bits;
+  const int heads = KV ? p.Hk : p.Hq, n_tiles = blocks / (p.B * heads);
+  const int ti = block / (p.B * heads), bh = block % (p.B * heads);
   const int x0 = (KV ? ti : n_tiles - 1 - ti) * 128;
   const int b = bh / heads, hx = bh % heads;
   const BatchMask mask = batch_mask(p.mask, b);
@@ -170,7 +186,11 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{p.err, abort_flag, p.timeout_ns};
   const int t_lo = range[0], per_head = max(0, range[1] - range[0]), whole0 = range[2], whole1 = range[3];
-  const int N = KV ? per_head * p.G : per_head;   // stream tiles
+  // stream tiles: the split's share of those of all heads, one head's behind the other's
+  const long all = static_cast<long>(per_head) * (KV ? p.G : 1);
+  const int n0 = static_cast<int>(all * split >> split_bits), N1 = static_cast<int>(all * (split + 1) >> split_bits) - n0;
+  const int N0 = TWICE ? N1 : 0;                  // steps that only sum
+  const int N = N0 + N1;
 
   if (warp >= Cfg::LOADS) {
     if (warp == Cfg::LOADS) {
@@ -190,7 +210,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
         for (int n = 0; n < N; ++n) {
           const int st = n % NST;
           if (n >= NST && !mbar_wait(y_empty + st, (n / NST - 1) & 1, wc)) break;
-          const int g = KV ? n / per_head : 0, row = (t_lo + n - g * per_head) * T;
+          const int g = KV ? (n0 + n) / per_head : 0, row = (t_lo + (KV ? n0 + n - g * per_head : n < N0 ? n : n - N0)) * T;
           const int hy = KV ? hx * p.G + g : hx / p.G;
           mbar_arrive_expect_tx(y_full + st, 2 * Cfg::Y_B + (KV ? Cfg::R_B : 0));
           Tile::load(sy + 2 * st * Cfg::Y_B, &tm_y1, y_full + st, row, hy, b, T);
@@ -245,12 +265,13 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
           if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < T / 16; ++ks)
-              umma_ts(tmem + Cfg::COL_OUT1, col + T + a_col(ks), y1 + ks * Tile::KSTEP_MN, idesc_o, (n > 0 || ks > 0) ? 1u : 0u);
+              if (n >= N0)
+                umma_ts(tmem + Cfg::COL_OUT1, col + T + a_col(ks), y1 + ks * Tile::KSTEP_MN, idesc_o, (n > N0 || ks > 0) ? 1u : 0u);
 #pragma unroll
             for (int ks = 0; ks < T / 16; ++ks) {
               if (KV)
                 umma_ts(tmem + Cfg::COL_OUT2, col + a_col(ks), y2 + ks * Tile::KSTEP_MN, idesc_o, (n > 0 || ks > 0) ? 1u : 0u);
-              else   // the low parts of dS
+              else if (n >= N0)   // the low parts of dS
                 umma_ts(tmem + Cfg::COL_OUT1, col + a_col(ks), y1 + ks * Tile::KSTEP_MN, idesc_o, 1u);
             }
             umma_commit(y_empty + st);
@@ -288,7 +309,8 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
       }
       if (MOD == 2) slope2 = p.slopes[hx] * kLog2e;
     }
-    uint64_t delta2 = f2_dup(0.f), total2 = delta2;  // dQ pass: sums of P g and (bias) of P
+    constexpr bool SUM_P = !KV && (MOD == 2 || TWICE);
+    uint64_t delta2 = f2_dup(0.f), total2 = delta2;  // dQ pass: sums of P g and (SUM_P) of P
     bool ok = true;
     if (Cfg::XT && N > 0) {   // this lane's row of X1 (the first half of the warpgroups) or X2 into TMEM
       constexpr int EACH = 2 * D / Cfg::WGS;          // elements a warpgroup brings
@@ -314,10 +336,44 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
       tc_fence_before();
       mbar_arrive_warp(x_full);
     }
-    int g = 0, tn = Cfg::SHARE ? 0 : w;               // query head of the key head, tile of that head's stream
-    for (int n = tn; n < N; n += Cfg::SHARE ? 1 : 2, tn += Cfg::SHARE ? 1 : 2) {
+    // query head of the key head, tile of that head's stream
+    int g = KV && n0 > 0 ? n0 / per_head : 0, tn = n0 - g * per_head + (Cfg::SHARE ? 0 : w);
+    // dQ pass, once per thread: the warpgroups' sums, and delta and l2 as they
+    // come out, for the dK/dV pass
+    float inv_total = 1.f;
+    auto settle = [&] {
+      float d0, d1, t0, t1;
+      f2_unpack(delta2, d0, d1);
+      f2_unpack(total2, t0, t1);
+      float2* share = reinterpret_cast<float2*>(sr);
+      share[w * 128 + tid] = make_float2(d0 + d1, t0 + t1);
+      named_bar_sync(1, 128 * Cfg::WGS);
+      float2 a = share[tid];
+#pragma unroll
+      for (int i = 1; i < Cfg::WGS; ++i) {
+        const float2 c = share[128 * i + tid];
+        a.x += c.x;
+        a.y += c.y;
+      }
+      const float total = SUM_P ? a.y : 1.f;
+      inv_total = total > 0.f ? 1.f / total : total;   // NaN stays
+      if (nl2 != -INFINITY) {
+        ndelta = -a.x * inv_total;
+        if (w == 0 && row < p.mask.Nq) {
+          stat[0] = nl2 - log2f(total);
+          stat[TR] = ndelta;
+        }
+      }
+    };
+    bool settled = KV;
+    for (int n = Cfg::SHARE ? 0 : w; n < N; n += Cfg::SHARE ? 1 : 2, tn += Cfg::SHARE ? 1 : 2) {
       if (KV)
         for (; tn >= per_head; tn -= per_head) ++g;
+      if (TWICE && !settled && n >= N0) {
+        settle();
+        settled = true;
+        tn -= N0;
+      }
       const int st = n % NST, buf = n & 1;
       const uint32_t col_s = lane_base + Cfg::COL_S + buf * 2 * T + c0, col_g = col_s + T;
       const int y0 = (t_lo + tn) * T;
@@ -346,6 +402,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
       // one body for tiles that every row sees whole, one for the others
       auto tile = [&](auto whole) {
         constexpr bool FULL = decltype(whole)::value;
+        constexpr bool AHEAD = MOD != 2;            // the next columns' read in flight; the bias needs those registers
         uint32_t s[2][CH], gg[2][CH];
         tmem_ld_cols<CH>(col_s, s[0]);
         tmem_ld_cols<CH>(col_g, gg[0]);
@@ -356,7 +413,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
         for (int c = 0; c < COLS; c += CH) {
           constexpr int NB = CH;
           const int cur = (c / CH) & 1;
-          if (c + CH < COLS) {   // the next columns' read in flight
+          if (AHEAD && c + CH < COLS) {
             tmem_ld_cols<NB>(col_s + c + CH, s[cur ^ 1]);
             tmem_ld_cols<NB>(col_g + c + CH, gg[cur ^ 1]);
           }
@@ -439,7 +496,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
                 pk[q + u] = pack_bf16x2(p0, p1);
               } else {
                 delta2 = f2_add(delta2, pg);
-                if (MOD == 2) total2 = f2_add(total2, f2_pack(p0, p1));
+                if (SUM_P) total2 = f2_add(total2, f2_pack(p0, p1));
                 f2_unpack(f2_fma(f2_pack(bf16_lo(hi16), bf16_hi(hi16)), f2_dup(-1.f), ds), s0, s1);
                 dl[q + u] = pack_bf16x2(s0, s1);
               }
@@ -448,6 +505,10 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
           tmem_st_cols<CH / 2>(col_s + c / 2, KV ? pk : dl);
           tmem_st_cols<CH / 2>(col_g + c / 2, dk);
           if (c + CH < COLS) {
+            if (!AHEAD) {
+              tmem_ld_cols<NB>(col_s + c + CH, s[cur ^ 1]);
+              tmem_ld_cols<NB>(col_g + c + CH, gg[cur ^ 1]);
+            }
             tmem_wait_ld();
             regs_loaded(s[cur ^ 1]);
             regs_loaded(gg[cur ^ 1]);
@@ -467,31 +528,10 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
       tc_fence_before();
       mbar_arrive_warp(p_full + buf);
     }
-    float inv_total = 1.f;
-    if (!KV) {   // the warpgroups' shares; delta and l2 as they come out, for the dK/dV pass
-      float d0, d1, t0, t1;
-      f2_unpack(delta2, d0, d1);
-      f2_unpack(total2, t0, t1);
-      float2* share = reinterpret_cast<float2*>(sr);
-      share[w * 128 + tid] = make_float2(d0 + d1, t0 + t1);
-      named_bar_sync(1, 128 * Cfg::WGS);
-      float2 a = share[tid];
-#pragma unroll
-      for (int i = 1; i < Cfg::WGS; ++i) {
-        const float2 c = share[128 * i + tid];
-        a.x += c.x;
-        a.y += c.y;
-      }
-      const float total = MOD == 2 ? a.y : 1.f;
-      inv_total = total > 0.f ? 1.f / total : total;   // NaN stays
-      if (w == 0 && row < p.mask.Nq && nl2 != -INFINITY) {
-        stat[0] = nl2 - log2f(total);
-        stat[TR] = -a.x * inv_total;
-      }
-    }
+    if (!settled) settle();                           // (TWICE: after an abort, or if the second sweep has no tile for it)
     if (ok && N > 0) ok = mbar_wait_warp(all_done, 0, wc);
     ok = __all_sync(~0u, ok);
-    if (ok) {
+    if (ok || splits > 1) {
       tc_fence_after();
       // the outputs' columns are dealt to the warpgroups, 16 at least each: dK then dV, or dQ
       constexpr int OUT = Cfg::OUTS * D, EACH = OUT / Cfg::WGS < 16 ? 16 : OUT / Cfg::WGS;
@@ -508,10 +548,19 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
                                       : nl2 == -INFINITY);
       for (int d = d_beg; d < d_end; d += 16) {
         uint32_t o[16];
-        if (N > 0) {
+        if (N > 0 && ok) {
           tmem_ld16(col + d, o);
           tmem_wait_ld();
           regs_loaded(o);
+        }
+        if (KV && splits > 1) {
+          float4* part = reinterpret_cast<float4*>(reinterpret_cast<float*>(sm) + tid * Cfg::PART + (second ? D : 0) + d);
+          const bool some = N > 0 && ok;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            part[i] = some ? make_float4(as_f(o[4 * i]), as_f(o[4 * i + 1]), as_f(o[4 * i + 2]), as_f(o[4 * i + 3]))
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+          continue;
         }
         uint32_t pk[8];
 #pragma unroll
@@ -527,6 +576,29 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
   }
   tc_fence_before();
   __syncthreads();
+  if (KV && splits > 1) {   // each CTA of the cluster adds up its share of the rows, in the splits' order
+    cluster_sync();
+    const int per = 128 / splits;
+    for (int i = threadIdx.x; i < per * (2 * D / 8); i += Cfg::THREADS) {
+      const int r = split * per + i / (2 * D / 8), c = 8 * (i % (2 * D / 8)), row = x0 + r;
+      if (row >= p.mask.Nk) continue;
+      float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+      const float* part = reinterpret_cast<const float*>(sm) + r * Cfg::PART + c;
+      for (int k = 0; k < splits; ++k) {
+        const float4 a = peer_load4(peer_smem(part, k)), e = peer_load4(peer_smem(part + 4, k));
+        u = make_float4(u.x + a.x, u.y + a.y, u.z + a.z, u.w + a.w);
+        v = make_float4(v.x + e.x, v.y + e.y, v.z + e.z, v.w + e.w);
+      }
+      const bool zero = all == 0 || row >= mask.len || (mask.doc && mask.doc[row].x == mask.doc[row].y);
+      const float f = c >= D ? 1.f : p.scale;
+      uint16_t* out = c >= D ? bp.dv + b * bp.dvs[0] + hx * bp.dvs[1] + static_cast<long>(row) * bp.dvs[2] + c - D
+                             : bp.dk + b * bp.dks[0] + hx * bp.dks[1] + static_cast<long>(row) * bp.dks[2] + c;
+      *reinterpret_cast<uint4*>(out) =
+          zero ? make_uint4(0, 0, 0, 0) : make_uint4(pack_bf16x2(u.x * f, u.y * f), pack_bf16x2(u.z * f, u.w * f),
+                                                     pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+    }
+    cluster_sync();         // the others have read this CTA's rows
+  }
   if (warp == Cfg::LOADS && lane == 0 && N > 0) {   // copies still in flight (only after an abort) must land before exit
     for (int st = 0; st < NST; ++st)
       if (last_load[st] >= 0) mbar_wait_drain(y_full + st, (last_load[st] / NST) & 1, p.timeout_ns);
@@ -538,27 +610,45 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
   }
 }
 
+// Splits of a key tile's stream in the dK/dV pass, as a power of two: as many
+// as leave no CTA without an SM, with two tiles each or more.  Without (with)
+// them, D = 128, causal: one key head of 8 query heads, 4096 rows, 477 us (135);
+// D = 32: 8 heads of 64 keys under 8192 rows 150 us (30), 8 heads of 2000 rows
+// 32 us (25).
+inline int bwd_split_bits(long ctas, int per_sm, long stream) {
+  int n = 0;
+  while ((2 << n) <= kAttnClusterSplits && (ctas << (n + 1)) <= kNumSM * per_sm && (4 << n) <= stream) ++n;
+  return n;
+}
+
 template <bool KV>
 cudaError_t launch_attn_bwd_pass(const CUtensorMap& x1, const CUtensorMap& x2, const CUtensorMap& y1,
                                  const CUtensorMap& y2, const AttnBwdParams& p, cudaStream_t s) {
   const long tiles = ((KV ? p.a.mask.Nk : p.a.mask.Nq) + 127) / 128;
-  const unsigned grid = static_cast<unsigned>(tiles * p.a.B * (KV ? p.a.Hk : p.a.Hq));
-  auto go = [&](auto d, auto mod) {
+  const long ctas = tiles * p.a.B * (KV ? p.a.Hk : p.a.Hq);
+  auto go = [&](auto d, auto mod, auto twice) {
     constexpr int D = decltype(d)::value;
     using C = BwdCfg<D, KV>;
-    auto* kern = attn_bwd_kernel<D, KV, decltype(mod)::value>;
+    auto* kern = attn_bwd_kernel<D, KV, decltype(mod)::value, decltype(twice)::value>;
     // at most CTAS CTAs share an SM, so that each finds its TMEM columns free
     constexpr int floor = 228 * 1024 / (C::CTAS + 1) + 1024;
     constexpr int smem = C::BYTES + 1024 > floor ? C::BYTES + 1024 : floor;
-    const cudaError_t e = allow_smem<std::pair<C, decltype(mod)>>(kern, smem);
+    const cudaError_t e = allow_smem<std::tuple<C, decltype(mod), decltype(twice)>>(kern, smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, C::THREADS, smem, s>>>(x1, x2, y1, y2, p);
-    return cudaGetLastError();
+    AttnBwdParams q = p;
+    q.split_bits = KV ? bwd_split_bits(ctas, C::CTAS, static_cast<long>(p.a.G) * ((p.a.mask.Nq + C::T - 1) / C::T)) : 0;
+    return launch_splits(kern, dim3(static_cast<unsigned>(ctas << q.split_bits)), C::THREADS, smem, s,
+                         dim3(1u << q.split_bits), 1 << q.split_bits, x1, x2, y1, y2, q);
+  };
+  auto by_sweeps = [&](auto d, auto mod) {
+    if constexpr (!KV)
+      if (p.a.mask.Nk <= kAttnTwiceKeys) return go(d, mod, std::true_type{});
+    return go(d, mod, std::false_type{});
   };
   auto by_mod = [&](auto d) {
-    return p.a.slopes      ? go(d, std::integral_constant<int, 2>{})
-           : p.a.cap > 0.f ? go(d, std::integral_constant<int, 1>{})
-                           : go(d, std::integral_constant<int, 0>{});
+    return p.a.slopes      ? by_sweeps(d, std::integral_constant<int, 2>{})
+           : p.a.cap > 0.f ? by_sweeps(d, std::integral_constant<int, 1>{})
+                           : by_sweeps(d, std::integral_constant<int, 0>{});
   };
   switch (p.a.D) {
     case 16: return by_mod(std::integral_constant<int, 16>{});

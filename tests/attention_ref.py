@@ -7,13 +7,16 @@ fp32 operations behind them move a score by at most `ds`; weights are
 exponentials of scores (an absolute error of a score is a relative error of its
 weight) rounded to bf16 where they enter a product, with an fp32 sum of up to
 Nk terms; outputs are rounded to bf16 once.  The backward's delta takes the
-rounded Y, its dS enters a product in bf16.
+rounded Y, its dS enters a product in bf16.  A weight below 2^-126, the smallest
+normal fp32 number (TINY), may come out as zero: an absolute error of up to TINY
+of each weight that a row sees.  Subnormal outputs are a multiple of 2^-133,
+which is less than TINY.
 """
 import math
 
 import torch
 
-STEP, HALF = 2.0 ** -24, torch.finfo(torch.bfloat16).eps / 2
+STEP, HALF, TINY = 2.0 ** -24, torch.finfo(torch.bfloat16).eps / 2, torch.finfo(torch.float32).tiny
 
 
 def visible(B, Nq, Nk, dev, lengths=None, q_lengths=None, q_offsets=None, documents=None, prefix=None, causal=False):
@@ -81,7 +84,8 @@ def attention(Q, K, V, dY=None, slopes=None, scale=0.0, cap=0.0, **masks):
     L = torch.logsumexp(s, -1, keepdim=True)
     P = torch.exp(s - torch.where(some, L, 0.0))
     y = P @ v
-    ytol = HALF * y.abs() + (HALF + 2 * eps) * (P @ v.abs()) * (1 + HALF)
+    seen = TINY * ok.double()
+    ytol = TINY + seen @ v.abs() + HALF * y.abs() + (HALF + 2 * eps) * (P @ v.abs()) * (1 + HALF)
     Lv = L.view(B, Hq, Nq)
     lt = torch.where(some, eps + 8 * STEP * (L.abs() + top.abs()), 0.0)
     if slopes is not None:
@@ -96,13 +100,14 @@ def attention(Q, K, V, dY=None, slopes=None, scale=0.0, cap=0.0, **masks):
     gerr = (D + 8) * STEP * (dy.abs() @ v.abs().transpose(-1, -2))
     derr = (dy.abs() * (ytol + (D + 8) * STEP * y.abs())).sum(-1, keepdim=True)
     E = P * (((g - delta).abs() * (HALF + e1) + gerr + derr) * dx + (g - delta).abs() * ddx) * (1 + HALF)
+    E = E + seen * (g - delta).abs()
     dq = scale * (dS @ k)
-    dqt = HALF * dq.abs() + scale * ((E + Nk * STEP * dS.abs()) @ k.abs()) * (1 + HALF)
+    dqt = TINY + HALF * dq.abs() + scale * ((E + Nk * STEP * dS.abs()) @ k.abs()) * (1 + HALF)
     n = G * Nq * STEP
     dk = scale * (dS.transpose(-1, -2) @ q).sum(2)
-    dkt = HALF * dk.abs() + scale * ((E + n * dS.abs()).transpose(-1, -2) @ q.abs()).sum(2) * (1 + HALF)
+    dkt = TINY + HALF * dk.abs() + scale * ((E + n * dS.abs()).transpose(-1, -2) @ q.abs()).sum(2) * (1 + HALF)
     dv = (P.transpose(-1, -2) @ dy).sum(2)
-    dvt = HALF * dv.abs() + ((P * (HALF + e1 + n)).transpose(-1, -2) @ dy.abs()).sum(2) * (1 + HALF)
+    dvt = TINY + HALF * dv.abs() + ((P * (HALF + e1 + n) + seen).transpose(-1, -2) @ dy.abs()).sum(2) * (1 + HALF)
     out.update(dQ=(dq.view(B, Hq, Nq, D), dqt.view(B, Hq, Nq, D)), dK=(dk, dkt), dV=(dv, dvt))
     return out
 

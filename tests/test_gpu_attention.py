@@ -120,6 +120,26 @@ def test_against_definition(name, D):
     check(*make(B, Hq, Hk, Nq, Nk, D, seed=D + Nq, layout="head" if D == 64 else "packed", **options(o, B, Nk)))
 
 
+# Backward where CTAs share a key tile's rows (few key heads, many rows), where none does, and either side of the
+# number of keys up to which the dQ pass sums twice.
+BACKWARD = {
+    "one_key_head": (1, 8, 1, 700, 300, {"cap": 9.0}),
+    "one_key_head_causal": (1, 6, 1, 1300, 1300, {"causal": True, "documents": ((500, 777), ())}),
+    "latents_ragged": (2, 2, 2, 3000, 40, {"lengths": (40, 17), "q_lengths": (2999, 3), "bias": True}),
+    "one_batch_idle": (3, 2, 1, 600, 70, {"q_lengths": (600, 0, 0), "lengths": (70, 70, 0)}),
+    "many_heads": (2, 16, 8, 300, 1300, {"lengths": (1300, 1111), "bias": True}),
+    "keys_1024": (1, 3, 1, 200, 1024, {"causal": True, "q_offsets": (824,)}),
+    "keys_1025": (1, 3, 1, 200, 1025, {"causal": True, "q_offsets": (824,)}),
+}
+
+
+@pytest.mark.parametrize("D", [16, 32, 64, 128])
+@pytest.mark.parametrize("name", BACKWARD)
+def test_backward_shapes(name, D):
+    B, Hq, Hk, Nq, Nk, o = BACKWARD[name]
+    check(*make(B, Hq, Hk, Nq, Nk, D, seed=D + Nk, **options(o, B, Nk)))
+
+
 @pytest.mark.parametrize("D", [16, 32, 64, 128])
 @pytest.mark.parametrize("G,Nq", [(1, 1), (4, 1), (3, 5), (16, 1), (1, 16), (2, 3)])
 @pytest.mark.parametrize("Nk", [1, 15, 16, 700, 5003])
