@@ -88,10 +88,28 @@ def call(name, where, dev, stream, *args):
         raise b.FlareError(st, where)
 
 
-def workspace(ws, nbytes, like):
+def empty(stream, *args, **kwargs):
+    """torch.empty whose memory is not handed out again before the work on
+    `stream` (None: the current one) that was enqueued by then is done."""
+    t = torch.empty(*args, **kwargs)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def output(name, t, like, dev, stream, check):
+    """An output of `like`'s shape, new unless given, and its pointer and strides."""
+    if t is None:
+        t = empty(stream, like.shape, dtype=_bf16, device=like.device)
+    elif check:
+        return t, check_rows(name, t, like.shape, dev, output=True)
+    return t, rows(t)
+
+
+def workspace(ws, nbytes, like, stream):
     """The caller's workspace, checked, or a new one."""
     if ws is None:
-        return torch.empty(nbytes if nbytes > 256 else 256, dtype=torch.uint8, device=like.device)
+        return empty(stream, nbytes if nbytes > 256 else 256, dtype=torch.uint8, device=like.device)
     check_small("workspace", ws, torch.uint8, None, like.get_device())
     if ws.numel() < nbytes:
         raise ValueError(f"workspace has {ws.numel()} bytes, needs {nbytes}")

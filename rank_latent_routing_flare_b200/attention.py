@@ -12,9 +12,11 @@ import functools
 import struct
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _binding as b
-from ._rows import NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, entry, ptr, rows, workspace as _ws
+from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, empty, entry, output as _output, ptr, rows,
+                    workspace as _ws)
 
 # flare_attention_args
 _ARGS = struct.Struct("=7q2d12q6q4qq4q12q")
@@ -62,23 +64,14 @@ def _device_check(device_check, ws, stream, where):
             raise b.FlareError(st, where + " (device status)")
 
 
-def _output(name, t, like, dev, check):
-    """An output of `like`'s shape, new unless given, and its pointer and strides."""
-    if t is None:
-        t = torch.empty_like(like, memory_format=torch.contiguous_format)
-    elif check:
-        return t, check_rows(name, t, like.shape, dev, output=True)
-    return t, rows(t)
-
-
 def _forward(where, Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap, Y, L,
              workspace, stream, check, device_check):
     head, sizes, dev = _head(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap,
                              check)
-    Y, y = _output("Y", Y, Q, dev, check)
+    Y, y = _output("Y", Y, Q, dev, stream, check)
     if check:
         check_small("L", L, _f32, Q.shape[:3], dev)
-    ws = _ws(workspace, flare_attention_workspace_bytes(*sizes), Q)
+    ws = _ws(workspace, flare_attention_workspace_bytes(*sizes), Q, stream)
     args = _ARGS.pack(*head, *y, ptr(L), *NO_ROWS, *NO_ROWS, *NO_ROWS, *NO_ROWS)
     call("flare_attention_fwd", where, dev, stream, args, ws.data_ptr(), ws.numel())
     _device_check(device_check, ws, stream, where)
@@ -111,7 +104,7 @@ def flare_attention_fwd_train(Q, K, V, lengths=None, q_lengths=None, q_offsets=N
                               slopes=None, causal: bool = False, scale: float = 0.0, cap: float = 0.0, Y=None,
                               L_out=None, workspace=None, stream=None, check: bool = True, device_check: bool = False):
     """flare_attention_fwd that returns (Y, L), what flare_attention_bwd takes."""
-    L = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device) if L_out is None else L_out
+    L = empty(stream, Q.shape[:3], dtype=torch.float32, device=Q.device) if L_out is None else L_out
     Y = _forward("flare_attention_fwd_train", Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes,
                  causal, scale, cap, Y, L, workspace, stream, check, device_check)
     return Y, L
@@ -132,10 +125,10 @@ def flare_attention_bwd(Q, K, V, Y, L, dY, lengths=None, q_lengths=None, q_offse
         check_small("L", L, _f32, Q.shape[:3], dev)
     else:
         y, dy = rows(Y), rows(dY)
-    dQ, dq = _output("dQ", dQ, Q, dev, check)
-    dK, dk = _output("dK", dK, K, dev, check)
-    dV, dv = _output("dV", dV, K, dev, check)
-    ws = _ws(workspace, flare_attention_workspace_bytes(*sizes, backward=True), Q)
+    dQ, dq = _output("dQ", dQ, Q, dev, stream, check)
+    dK, dk = _output("dK", dK, K, dev, stream, check)
+    dV, dv = _output("dV", dV, K, dev, stream, check)
+    ws = _ws(workspace, flare_attention_workspace_bytes(*sizes, backward=True), Q, stream)
     args = _ARGS.pack(*head, *y, L.data_ptr(), *dy, *dq, *dk, *dv)
     call("flare_attention_bwd", "flare_attention_bwd", dev, stream, args, ws.data_ptr(), ws.numel())
     _device_check(device_check, ws, stream, "flare_attention_bwd")
@@ -156,6 +149,7 @@ class Attention(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         Q, K, V, Y, L, *masks = ctx.saved_tensors
         dY = dY.to(torch.bfloat16).contiguous()

@@ -24,9 +24,9 @@ namespace {
 flare_status check_sizes(int64_t B, int64_t Hq, int64_t Hk, int64_t Nq, int64_t Nk, int64_t D) {
   if (B < 1 || Hq < 1 || Hk < 1 || Nq < 1 || Nk < 1 || Hq % Hk != 0) return FLARE_ERR_SHAPE;
   if (!row_width_ok(D)) return FLARE_ERR_UNSUPPORTED;
-  constexpr int64_t most = int64_t(1) << 30;
+  constexpr int64_t most = int64_t(1) << 27;   // a query tile of a CTA waits for the keys of the other: half a second at most
   if (Nq > most || Nk > most || B > 65535 || Hq > 65535) return FLARE_ERR_UNSUPPORTED;
-  // one CTA for 128 rows of a head at least, eight rows a CTA where splits are joined
+  // a CTA has eight rows of a head at least
   if (B * Hq * ((Nq + 7) / 8) > kMaxInt || B * Hk * ((Nk + 127) / 128) > kMaxInt) return FLARE_ERR_UNSUPPORTED;
   return FLARE_OK;
 }
@@ -94,8 +94,9 @@ bool map_rows(CUtensorMap* m, const void* base, const long (&st)[3], int64_t B, 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   // a thread that has made no CUDA call yet (a backward's) has no context
-  // current, which a runtime call mends
-  return encode() || (cudaFree(nullptr) == cudaSuccess && encode());
+  // current, which setting its device mends (during a capture too)
+  int dev;
+  return encode() || (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode());
 }
 
 // Rows that TMA reads: no broadcast (zero stride).
@@ -117,6 +118,7 @@ flare_status fill_common(const flare_attention_args* a, bool backward, const voi
   if (!a->Q || !a->K || !a->V || !a->Y || !ws) return FLARE_ERR_NULL;
   if (a->prefix && !a->causal) return FLARE_ERR_SHAPE;
   if (!std::isfinite(a->scale) || !std::isfinite(a->cap)) return FLARE_ERR_SHAPE;
+  if (a->cap > 0.0 && (a->cap < 1e-6 || a->cap > 1e9)) return FLARE_ERR_UNSUPPORTED;   // what the tanh is accurate for
   st = tma_strides(r->q, a->Q, a->q_stride, a->B, a->Hq, a->Nq, a->D);
   if (st == FLARE_OK) st = tma_strides(r->k, a->K, a->k_stride, a->B, a->Hk, a->Nk, a->D);
   if (st == FLARE_OK) st = tma_strides(r->v, a->V, a->v_stride, a->B, a->Hk, a->Nk, a->D);

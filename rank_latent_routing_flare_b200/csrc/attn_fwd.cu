@@ -572,17 +572,22 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
   }
 }
 
-// Join of the splits of one row (one warp a row): weights 2^(l_s - max).
+// Join of the splits of one row: weights 2^(l_s - max).  Eight warps take the
+// splits in turn (one warp's loads would wait for one another: 13 splits of 512
+// rows 7 us, so 5).
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
-  const long rows = static_cast<long>(p.B) * p.Hq * p.mask.Nq;
-  const long at = static_cast<long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (at >= rows) return;
-  const int lane = threadIdx.x & 31;
+  constexpr int WARPS = 8;
+  __shared__ float part[WARPS][129];
+  const long rows = static_cast<long>(p.B) * p.Hq * p.mask.Nq, at = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float top = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_l[s * rows + at]);
+  for (int s = lane; s < p.splits; s += 32) top = fmaxf(top, p.part_l[s * rows + at]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
   const float base = top == -INFINITY ? 0.f : top;
   float total = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < p.splits; ++s) {
+#pragma unroll 4
+  for (int s = warp; s < p.splits; s += WARPS) {
     const float w = ex2_mufu(p.part_l[s * rows + at] - base);
     total += w;
     const float* o = p.part_o + (s * rows + at) * p.D;
@@ -590,23 +595,39 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
     for (int i = 0; i < 4; ++i)
       if (lane + 32 * i < p.D) acc[i] = fmaf(w, o[lane + 32 * i], acc[i]);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) part[warp][lane + 32 * i] = acc[i];
+  if (lane == 0) part[warp][128] = total;
+  __syncthreads();
+  const int d = threadIdx.x;
+  if (d >= p.D) return;
+  float x = 0.f;
+  total = 0.f;
+#pragma unroll
+  for (int k = 0; k < WARPS; ++k) {
+    total += part[k][128];
+    x += part[k][d];
+  }
   const int n = static_cast<int>(at % p.mask.Nq);
   const long bh = at / p.mask.Nq;
   const int b = static_cast<int>(bh / p.Hq), h = static_cast<int>(bh % p.Hq);
-  uint16_t* y = p.y + b * p.ys[0] + h * p.ys[1] + n * p.ys[2];
-  const float inv = total == 0.f ? 0.f : 1.f / total;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (lane + 32 * i < p.D) y[lane + 32 * i] = static_cast<uint16_t>(pack_bf16x2(acc[i] * inv, 0.f));
-  if (lane == 0 && p.L) p.L[at] = natural_lse(p, batch_mask(p.mask, b), h, n, total == 0.f ? -INFINITY : top + log2f(total));
+  p.y[b * p.ys[0] + h * p.ys[1] + n * p.ys[2] + d] =
+      static_cast<uint16_t>(pack_bf16x2(total == 0.f ? 0.f : x * (1.f / total), 0.f));
+  if (d == 0 && p.L) p.L[at] = natural_lse(p, batch_mask(p.mask, b), h, n, total == 0.f ? -INFINITY : top + log2f(total));
 }
 
 // Documents: the start and the end of the run of equal ids each position lies
 // in (the start twice where the id is negative).  A CTA takes 1024 positions:
-// a bit for each that begins a run, then the nearest bit on either side; the
+// a bit for each that begins a run, then the nearest bit on either side.  The
 // ends of runs that reach into other chunks are searched for in the ids, 1024
-// at a time, so that no CTA waits on another.
-constexpr int kDocThreads = 256, kDocChunk = 1024;
+// at a time, where there are few chunks (ONE: one launch).  That is quadratic
+// in the chunks, so with many of them a first launch (SUMS) leaves each chunk's
+// last and first beginning in its first entry, a second turns them into what
+// lies before and behind each chunk, a third (ENDS) does the rest.  One
+// document, one launch (three): 8192 keys 13 us (11), 32768 36 (11), 2^20 1276 (22).
+constexpr int kDocThreads = 256, kDocChunk = 1024, kDocSearched = 8;   // chunks searched in one launch
+enum class Doc { ONE, SUMS, ENDS };
+template <Doc HOW>
 __global__ void __launch_bounds__(kDocThreads) attn_documents_kernel(const int32_t* ids, int2* doc, int N, int chunks) {
   __shared__ uint32_t bits[kDocChunk / 32];
   __shared__ int left, right;
@@ -620,40 +641,89 @@ __global__ void __launch_bounds__(kDocThreads) attn_documents_kernel(const int32
     if ((threadIdx.x & 31) == 0) bits[(k + threadIdx.x) / 32] = w;
   }
   if (threadIdx.x == 0) {
-    left = -1;
-    right = INT_MAX;
+    left = HOW == Doc::ENDS ? doc[c0].x : -1;
+    right = HOW == Doc::ENDS ? doc[c0].y : INT_MAX;
   }
   __syncthreads();
-  // the run that reaches into the chunk from the left, and the one out of it
-  for (int lo = c0; (bits[0] & 1u) == 0 && left < 0;) {
-    lo -= kDocChunk;   // 0 begins a run, so this ends
-    int at = -1;
-    for (int i = lo + static_cast<int>(threadIdx.x); i < lo + kDocChunk; i += kDocThreads)
-      if (i >= 0 && begins(i)) at = i;
-    __syncthreads();   // the loop's test of `left` is done
-    if (at >= 0) atomicMax(&left, at);
+  if constexpr (HOW == Doc::SUMS) {
+    if (threadIdx.x < kDocChunk / 32 && bits[threadIdx.x]) {
+      const int at = c0 + 32 * static_cast<int>(threadIdx.x);
+      atomicMax(&left, at + 31 - __clz(bits[threadIdx.x]));
+      atomicMin(&right, at + __ffs(bits[threadIdx.x]) - 1);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) doc[c0] = make_int2(left, right);
+  }
+  if constexpr (HOW == Doc::ONE) {   // the run that reaches into the chunk from the left, and the one out of it
+    for (int lo = c0; (bits[0] & 1u) == 0 && left < 0;) {
+      lo -= kDocChunk;   // 0 begins a run, so this ends
+      int at = -1;
+      for (int i = lo + static_cast<int>(threadIdx.x); i < lo + kDocChunk; i += kDocThreads)
+        if (i >= 0 && begins(i)) at = i;
+      __syncthreads();   // the loop's test of `left` is done
+      if (at >= 0) atomicMax(&left, at);
+      __syncthreads();
+    }
+    for (int lo = c0 + kDocChunk; right == INT_MAX; lo += kDocChunk) {
+      int at = INT_MAX;
+      for (int i = lo + kDocChunk - kDocThreads + static_cast<int>(threadIdx.x); i >= lo; i -= kDocThreads)
+        if (begins(i)) at = min(i, N);
+      __syncthreads();
+      if (at != INT_MAX) atomicMin(&right, at);
+      __syncthreads();
+    }
+  }
+  if constexpr (HOW != Doc::SUMS)
+    for (int k = threadIdx.x; k < kDocChunk; k += kDocThreads) {
+      const int i = c0 + k;
+      if (i >= N) break;
+      int w = k / 32;
+      uint32_t m = bits[w] & (~0u >> (31 - k % 32));          // bits up to k
+      while (m == 0 && w > 0) m = bits[--w];
+      const int start = m ? c0 + 32 * w + 31 - __clz(m) : left;
+      w = k / 32;
+      m = k % 32 == 31 ? 0u : bits[w] & (~0u << (k % 32 + 1));  // bits behind k
+      while (m == 0 && w < kDocChunk / 32 - 1) m = bits[++w];
+      const int end = m ? min(c0 + 32 * w + __ffs(m) - 1, N) : right;
+      doc[i] = make_int2(start, ids[i] < 0 ? start : end);
+    }
+}
+
+// A batch's chunks: (last, first beginning in the chunk) to (last beginning
+// before it, first one behind it).  One CTA, a range of chunks per thread.
+constexpr int kDocJoin = 1024;
+__global__ void __launch_bounds__(kDocJoin) attn_document_ends_kernel(int2* doc, int N, int chunks) {
+  __shared__ int last[kDocJoin], first[kDocJoin];
+  const int t = threadIdx.x, per = (chunks + kDocJoin - 1) / kDocJoin;
+  doc += static_cast<long>(blockIdx.x) * N;
+  const int beg = min(chunks, t * per), end = min(chunks, beg + per);
+  auto at = [&](int c) -> int2& { return doc[static_cast<long>(c) * kDocChunk]; };
+  int x = -1, y = N;
+  for (int c = beg; c < end; ++c) {
+    x = max(x, at(c).x);
+    y = min(y, at(c).y);
+  }
+  last[t] = x;
+  first[t] = y;
+  __syncthreads();
+  for (int o = 1; o < kDocJoin; o *= 2) {   // inclusive, from the left and from the right
+    const int a = t >= o ? last[t - o] : -1, z = t + o < kDocJoin ? first[t + o] : N;
+    __syncthreads();
+    last[t] = max(last[t], a);
+    first[t] = min(first[t], z);
     __syncthreads();
   }
-  for (int lo = c0 + kDocChunk; right == INT_MAX; lo += kDocChunk) {
-    int at = INT_MAX;
-    for (int i = lo + kDocChunk - kDocThreads + static_cast<int>(threadIdx.x); i >= lo; i -= kDocThreads)
-      if (begins(i)) at = min(i, N);
-    __syncthreads();
-    if (at != INT_MAX) atomicMin(&right, at);
-    __syncthreads();
+  x = t > 0 ? last[t - 1] : -1;
+  y = t + 1 < kDocJoin ? first[t + 1] : N;
+  for (int c = beg; c < end; ++c) {
+    const int here = at(c).x;
+    at(c).x = x;
+    x = max(x, here);
   }
-  for (int k = threadIdx.x; k < kDocChunk; k += kDocThreads) {
-    const int i = c0 + k;
-    if (i >= N) break;
-    int w = k / 32;
-    uint32_t m = bits[w] & (~0u >> (31 - k % 32));          // bits up to k
-    while (m == 0 && w > 0) m = bits[--w];
-    const int start = m ? c0 + 32 * w + 31 - __clz(m) : left;
-    w = k / 32;
-    m = k % 32 == 31 ? 0u : bits[w] & (~0u << (k % 32 + 1));  // bits behind k
-    while (m == 0 && w < kDocChunk / 32 - 1) m = bits[++w];
-    const int end = m ? min(c0 + 32 * w + __ffs(m) - 1, N) : right;
-    doc[i] = make_int2(start, ids[i] < 0 ? start : end);
+  for (int c = end - 1; c >= beg; --c) {
+    const int here = at(c).y;
+    at(c).y = y;
+    y = min(y, here);
   }
 }
 
@@ -661,7 +731,14 @@ __global__ void __launch_bounds__(kDocThreads) attn_documents_kernel(const int32
 
 cudaError_t launch_attn_documents(const int32_t* ids, int2* doc, int B, int N, cudaStream_t s) {
   const int chunks = (N + kDocChunk - 1) / kDocChunk;
-  attn_documents_kernel<<<static_cast<unsigned>(static_cast<long>(B) * chunks), kDocThreads, 0, s>>>(ids, doc, N, chunks);
+  const unsigned grid = static_cast<unsigned>(static_cast<long>(B) * chunks);
+  if (chunks <= kDocSearched) {
+    attn_documents_kernel<Doc::ONE><<<grid, kDocThreads, 0, s>>>(ids, doc, N, chunks);
+  } else {
+    attn_documents_kernel<Doc::SUMS><<<grid, kDocThreads, 0, s>>>(ids, doc, N, chunks);
+    attn_document_ends_kernel<<<static_cast<unsigned>(B), kDocJoin, 0, s>>>(doc, N, chunks);
+    attn_documents_kernel<Doc::ENDS><<<grid, kDocThreads, 0, s>>>(ids, doc, N, chunks);
+  }
   return cudaGetLastError();
 }
 
@@ -703,7 +780,7 @@ cudaError_t launch_attn_fwd(const AttnMaps& m, const AttnParams& p, cudaStream_t
 
 cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t s) {
   const long rows = static_cast<long>(p.B) * p.Hq * p.mask.Nq;
-  attn_join_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(p);
+  attn_join_kernel<<<static_cast<unsigned>(rows), 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 

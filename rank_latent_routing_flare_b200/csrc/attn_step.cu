@@ -15,6 +15,7 @@
 // split over CTAs, within a CTA over 8 warps, which join in shared memory; up
 // to eight splits are a cluster and join there too.
 #include <type_traits>
+#include <utility>
 
 #include "attn_common.cuh"
 #include "ops_internal.h"
@@ -86,7 +87,8 @@ __device__ __forceinline__ void load_chunk(Chunk<D>& c, const StepParams& p, con
   }
 }
 
-template <int D>
+// CAP: capped scores; without, the tanh's coefficients take no registers.
+template <int D, bool CAP>
 __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_kernel(const StepParams p) {
   using C = StepCfg<D>;
   extern __shared__ __align__(16) float sh[];   // [warps][rows] (m, l) pairs, then [warps][rows][D]
@@ -169,12 +171,27 @@ __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_k
         for (int n = 0; n < 2; ++n) mma16816(s[n], q, c.k[n][blk][2 * u], c.k[n][blk][2 * u + 1]);
       }
     float mx[2] = {-INFINITY, -INFINITY};
+    if (CAP) {
+      float top = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(s[0][k]), fabsf(s[1][k])));
+      if (__all_sync(~0u, ops.small(top))) {
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+          float* x = &s[k / 4][k % 4];
+          f2_unpack(ops.poly(f2_pack(x[0], x[1]), f2_dup(0.f)), x[0], x[1]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[k / 4][k % 4] = ops.capped(s[k / 4][k % 4]);
+      }
+    }
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int u = k >> 1, key = key0 + 8 * n + 2 * t + (k & 1);
-        float x = a.cap > 0.f ? ops.capped(s[n][k]) : s[n][k] * ops.c2;
+        float x = CAP ? s[n][k] : s[n][k] * ops.c2;
         if (a.slopes) x = fmaf(-slope2[u], fabsf(static_cast<float>(pos[u] - key)), x);
         if (key < iv[u].x || key >= iv[u].y) x = -INFINITY;
         s[n][k] = x;
@@ -312,20 +329,21 @@ cudaError_t launch_attn_step(const AttnParams& p, const AttnSide& q, const AttnS
   const StepParams sp{p, q, k, v};
   const dim3 grid(static_cast<unsigned>(static_cast<long>(p.splits) * p.B * p.Hk));
   const int rows = p.G * p.mask.Nq, smem = step_smem(rows, p.D);
-  auto go = [&](auto d) {
+  auto go = [&](auto d, auto cap) {
     constexpr int D = decltype(d)::value;
-    auto* kern = attn_step_kernel<D>;
+    auto* kern = attn_step_kernel<D, decltype(cap)::value>;
     if (smem > 48 * 1024) {
-      const cudaError_t e = allow_smem<StepCfg<D>>(kern, step_smem(kAttnStepRows, D));
+      const cudaError_t e = allow_smem<std::pair<StepCfg<D>, decltype(cap)>>(kern, step_smem(kAttnStepRows, D));
       if (e != cudaSuccess) return e;
     }
     return launch_splits(kern, grid, kStepWarps * 32, smem, s, dim3(p.splits, 1, 1), p.splits, sp);
   };
+  auto by_cap = [&](auto d) { return p.cap > 0.f ? go(d, std::true_type{}) : go(d, std::false_type{}); };
   switch (p.D) {
-    case 16: return go(std::integral_constant<int, 16>{});
-    case 32: return go(std::integral_constant<int, 32>{});
-    case 64: return go(std::integral_constant<int, 64>{});
-    case 128: return go(std::integral_constant<int, 128>{});
+    case 16: return by_cap(std::integral_constant<int, 16>{});
+    case 32: return by_cap(std::integral_constant<int, 32>{});
+    case 64: return by_cap(std::integral_constant<int, 64>{});
+    case 128: return by_cap(std::integral_constant<int, 128>{});
   }
   return cudaErrorInvalidValue;
 }

@@ -13,8 +13,10 @@ import functools
 import struct
 
 import torch
+from torch.autograd.function import once_differentiable
 
-from ._rows import NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, entry, ptr, rows, workspace as _ws
+from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, empty, entry, output as _output, ptr, rows,
+                    workspace as _ws)
 
 # flare_qk_norm_rope_args
 _ARGS = struct.Struct("=9qd3q4q4q2q2q4q4q4q4q2q")
@@ -83,17 +85,13 @@ def _head(Q, K, q_gain, k_gain, freqs, positions, lengths, eps, interleaved, che
     return packed, (B, N, D, Hq, Hk, dev)
 
 
-def _output(name, t, like, dev, check):
-    """An output of `like`'s shape, new unless given, and its pointer and strides."""
-    if like is None:
-        if t is not None:
-            raise ValueError(f"{name} is given without its input")
-        return None, NO_ROWS
-    if t is None:
-        t = torch.empty_like(like, memory_format=torch.contiguous_format)
-    elif check:
-        return t, check_rows(name, t, like.shape, dev, output=True)
-    return t, rows(t)
+def _side(name, t, like, dev, stream, check):
+    """The output that goes with an input, which may be absent."""
+    if like is not None:
+        return _output(name, t, like, dev, stream, check)
+    if t is not None:
+        raise ValueError(f"{name} is given without its input")
+    return None, NO_ROWS
 
 
 def flare_qk_norm_rope_fwd(Q=None, K=None, q_gain=None, k_gain=None, freqs=None, positions=None, lengths=None,
@@ -110,8 +108,8 @@ def flare_qk_norm_rope_fwd(Q=None, K=None, q_gain=None, k_gain=None, freqs=None,
     multiple of 16, or (2p, 2p + 1) when ``interleaved``.  Rows n >=
     lengths[b] (int32 [B]) are not read and come out as zeros."""
     head, (*_, dev) = _head(Q, K, q_gain, k_gain, freqs, positions, lengths, eps, interleaved, check)
-    Qr, q = _output("Qr", Qr, Q, dev, check)
-    Kr, k = _output("Kr", Kr, K, dev, check)
+    Qr, q = _side("Qr", Qr, Q, dev, stream, check)
+    Kr, k = _side("Kr", Kr, K, dev, stream, check)
     args = _ARGS.pack(*head, *q, *k, *NO_ROWS, *NO_ROWS, 0, 0)
     call("flare_qk_norm_rope_fwd", "flare_qk_norm_rope_fwd", dev, stream, args)
     return Qr, Kr
@@ -131,18 +129,19 @@ def flare_qk_norm_rope_bwd(Q=None, K=None, dQr=None, dKr=None, q_gain=None, k_ga
             raise ValueError(f"{name} goes with its input")
         dy += NO_ROWS if t is None else check_rows(name, t, x.shape, dev) if check else rows(t)
     g = dict(grads or {})
-    g["dQ"], q = _output("dQ", g.get("dQ"), Q, dev, check)
-    g["dK"], k = _output("dK", g.get("dK"), K, dev, check)
+    g["dQ"], q = _side("dQ", g.get("dQ"), Q, dev, stream, check)
+    g["dK"], k = _side("dK", g.get("dK"), K, dev, stream, check)
     for name, gain in (("dq_gain", q_gain), ("dk_gain", k_gain)):
         if gain is None:
             g[name] = None
         elif g.get(name) is None:
-            g[name] = torch.empty_like(gain)
+            g[name] = empty(stream, gain.shape, dtype=_f32, device=gain.device)
         elif check:
             check_small(name, g[name], _f32, gain.shape, dev)
     ws, nbytes = 0, 0
     if q_gain is not None or k_gain is not None:
-        workspace = _ws(workspace, flare_qk_norm_rope_workspace_bytes(B, N, Hq, Hk, D), Q if Q is not None else K)
+        workspace = _ws(workspace, flare_qk_norm_rope_workspace_bytes(B, N, Hq, Hk, D), Q if Q is not None else K,
+                        stream)
         ws, nbytes = workspace.data_ptr(), workspace.numel()
     args = _ARGS.pack(*head, *dy, *q, *k, ptr(g["dq_gain"]), ptr(g["dk_gain"]))
     call("flare_qk_norm_rope_bwd", "flare_qk_norm_rope_bwd", dev, stream, args, ws, nbytes)
@@ -162,6 +161,7 @@ class QkNormRope(torch.autograd.Function):
         return flare_qk_norm_rope_fwd(Q, K, q_gain, k_gain, freqs, positions, lengths, eps, interleaved)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dQr, dKr):
         Q, K, q_gain, k_gain, freqs, positions, lengths = ctx.saved_tensors
         g = flare_qk_norm_rope_bwd(Q, K, _dense(dQr, Q), _dense(dKr, K), q_gain, k_gain, freqs, positions, lengths,

@@ -63,6 +63,14 @@ def test_refusals(call):
     assert call(ws_bytes=need - 1) == Status.ERR_WORKSPACE
 
 
+@pytest.mark.parametrize("call", [fwd, bwd])
+def test_caps_and_lengths_out_of_range(call):
+    for over in (dict(cap=1e-7), dict(cap=1e10), dict(cap=1e-60), dict(Nk=(1 << 27) + 1), dict(Nq=(1 << 27) + 1)):
+        assert call(**over) == Status.ERR_UNSUPPORTED, over
+    for over in (dict(cap=1e-6), dict(cap=1e9), dict(cap=-1e30)):
+        assert call(**over) != Status.ERR_UNSUPPORTED, over
+
+
 def test_backward_refusals():
     for name in ("L", "dY", "dQ", "dK", "dV"):
         assert bwd(**{name: 0}) == Status.ERR_NULL, name
