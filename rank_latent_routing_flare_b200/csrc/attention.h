@@ -76,6 +76,7 @@ constexpr int kAttnStepRows = 16;   // query rows per key head of the kernel for
 cudaError_t launch_attn_step(const AttnParams& p, const AttnSide& q, const AttnSide& k, const AttnSide& v,
                              cudaStream_t s);
 
+int attn_step_ctas(int D);                  // CTAs of the few-row kernel that share an SM
 int attn_bwd_stream_tile(int D, bool kv);   // rows per streamed tile of the dQ pass and of the dK/dV pass
 bool attn_bwd_rows_in_tmem(int D, bool kv);  // whether a pass reads its own tile of rows without a map
 cudaError_t launch_attn_rows(const AttnBwdParams& p, cudaStream_t s);

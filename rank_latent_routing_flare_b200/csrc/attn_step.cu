@@ -2,18 +2,16 @@
 // cache.  A key head's query rows (its G query heads times Nq <= 16 rows)
 // share every key and value, so K and V are read once and the kernel is bound
 // by HBM; the products (m16n8k16 mma.sync, 16 rows at a time) are far below
-// the tensor pipe's rate and take registers as they come from global memory.
+// the tensor pipe's rate.
 //
-// Each warp streams chunks of 16 keys, 16-byte loads straight into the
-// operand fragments, the next chunk's loads in flight while one is computed:
-//  - scores: a lane's 8 consecutive elements of a K row feed two k-steps; the
-//    order of D inside a dot product is free, and Q's fragments use the same.
-//  - values: lane (g, t) reads elements 8g .. 8g+7 of the four V rows 2t, 2t+1,
-//    2t+8, 2t+9 and pairs rows with byte permutes; output column n of product i
-//    is element 8n + i.
+// Each warp streams chunks of 16 keys through a ring of its own in shared
+// memory (16-byte cp.async, rows swizzled so that ldmatrix meets no bank
+// conflict): what is in flight takes no registers, so that several CTAs of
+// four warps share an SM and one's beginning and end run under the others'
+// loads.  K's fragments come from ldmatrix, V's from its transposing form.
 // Rows keep a running reference and sum as in the tiled kernel.  The keys are
-// split over CTAs, within a CTA over 8 warps, which join in shared memory; up
-// to eight splits are a cluster and join there too.
+// split over CTAs, within a CTA over its warps, which join in shared memory;
+// up to eight splits are a cluster and join there too.
 #include <type_traits>
 #include <utility>
 
@@ -23,7 +21,7 @@
 namespace flare {
 namespace {
 
-constexpr int kStepWarps = 8, kChunk = 16;
+constexpr int kStepWarps = 4, kChunk = 16;
 
 struct StepParams {
   AttnParams a;
@@ -32,23 +30,28 @@ struct StepParams {
 
 template <int D>
 struct StepCfg {
-  static constexpr int KB = D >= 32 ? D / 32 : 1;   // loads per K row and lane
-  static constexpr int KE = D >= 32 ? 8 : 4;        // elements per load
-  static constexpr int VE = D >= 64 ? 8 : D / 8;
-  static constexpr int VB = D / (8 * VE);
+  static constexpr int U = D / 8;                       // 16-byte units of a row
+  static constexpr int CHUNK_B = kChunk * D * 2;        // K's or V's part of a chunk
+  static constexpr int STAGES = D == 128 ? 2 : D == 64 ? 3 : 4;
+  static constexpr int CTAS = D == 128 ? 3 : D == 64 ? 4 : 6;
+  static constexpr int RING_B = kStepWarps * STAGES * 2 * CHUNK_B;
+  // 16-byte unit u of row r of a chunk: eight rows of the same unit, and eight units of a row, lie in different banks
+  __device__ static constexpr int swizzle(int r) { return U >= 8 ? r & 7 : U == 4 ? r >> 1 & 3 : r >> 2 & 1; }
 };
 
-template <int N>   // words of 4 bytes
-__device__ __forceinline__ void load_words(const uint16_t* p, bool ok, uint32_t (&w)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) w[i] = 0u;
-  if (!ok) return;
-  if constexpr (N == 4)
-    asm("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
-  else if constexpr (N == 2)
-    asm("ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-  else
-    asm("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {   // zeros if not ok
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -56,42 +59,32 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Copies of a chunk's rows of K and V, zeros from key `end` on.
 template <int D>
-struct Chunk {
-  uint32_t k[2][StepCfg<D>::KB][StepCfg<D>::KE / 2];   // keys g and 8 + g
-  uint32_t v[4][StepCfg<D>::VB][StepCfg<D>::VE / 2];   // keys 2t, 2t+1, 2t+8, 2t+9
-};
-template <int D>
-__device__ __forceinline__ void load_chunk(Chunk<D>& c, const StepParams& p, const BatchMask& m, const uint16_t* kb,
+__device__ __forceinline__ void load_chunk(uint32_t dst, const StepParams& p, const BatchMask& m, const uint16_t* kb,
                                            const uint16_t* vb, int key0, int end) {
   using C = StepCfg<D>;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    const int key = key0 + 8 * n + g;
-#pragma unroll
-    for (int i = 0; i < C::KB; ++i)
-      load_words(kb + static_cast<long>(key) * p.k.sn + 32 * i + C::KE * t, key < end, c.k[n][i]);
-  }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int key = key0 + 2 * t + (r & 1) + 8 * (r >> 1);
-    bool ok = key < end;
+  for (int i = 0; i < kChunk * C::U / 32; ++i) {
+    const int e = lane + 32 * i, r = e / C::U, u = e % C::U, key = key0 + r;
+    const uint32_t at = dst + 2 * D * r + 16 * (u ^ C::swizzle(r));
+    const bool ok = key < end;
+    copy16(at, ok ? kb + static_cast<long>(key) * p.k.sn + 8 * u : kb, ok);
+    bool okv = ok;
     if (m.doc && ok) {   // a weight of 0 does not erase a NaN: padding inside the range is not read
       const int2 d = m.doc[key];
-      ok = d.x != d.y;
+      okv = d.x != d.y;
     }
-#pragma unroll
-    for (int i = 0; i < C::VB; ++i)
-      load_words(vb + static_cast<long>(key) * p.v.sn + 64 * i + C::VE * g, ok, c.v[r][i]);
+    copy16(at + C::CHUNK_B, okv ? vb + static_cast<long>(key) * p.v.sn + 8 * u : vb, okv);
   }
 }
 
 // CAP: capped scores; without, the tanh's coefficients take no registers.
 template <int D, bool CAP>
-__global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_kernel(const StepParams p) {
+__global__ void __launch_bounds__(kStepWarps * 32, StepCfg<D>::CTAS) attn_step_kernel(const StepParams p) {
   using C = StepCfg<D>;
-  extern __shared__ __align__(16) float sh[];   // [warps][rows] (m, l) pairs, then [warps][rows][D]
+  extern __shared__ __align__(128) uint8_t sh[];   // the warps' rings; behind the loop the join's data
   const AttnParams& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int split = blockIdx.x % a.splits, bk = blockIdx.x / a.splits, b = bk / a.Hk, hk = bk % a.Hk;
@@ -110,12 +103,23 @@ __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_k
   const int per = (chunks + a.splits - 1) / a.splits;
   const int c_end = min(chunks, (split + 1) * per);
 
+  const uint16_t* kb = p.k.p + b * p.k.sb + hk * p.k.sh;
+  const uint16_t* vb = p.v.p + b * p.v.sb + hk * p.v.sh;
+  const uint32_t ring = smem_u32(sh) + warp * C::STAGES * 2 * C::CHUNK_B;
+  const int c_beg = split * per + warp;
+  auto load = [&](int n) {   // the warp's chunk n
+    const int c = c_beg + n * kStepWarps;
+    if (c < c_end) load_chunk<D>(ring + n % C::STAGES * 2 * C::CHUNK_B, p, mask, kb, vb, lo + c * kChunk, hi);
+    copies_end();
+  };
+#pragma unroll
+  for (int n = 0; n < C::STAGES - 1; ++n) load(n);
+
   // this lane's two rows: r = i G + head
   int2 iv[2];
   int pos[2];
   float slope2[2];
   __shared__ uint4 sm_q[D / 16][32];   // Q's operand fragments, the same for every warp: read per chunk, they hold no registers
-  uint32_t qf[D / 16][4];
   const ScoreOps ops(a.scale, a.cap, true);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
@@ -125,51 +129,40 @@ __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_k
     pos[u] = bias_position(mask, have ? i : 0, iv[u]);
     slope2[u] = have && a.slopes ? a.slopes[h] * kLog2e : 0.f;
     const uint16_t* q = p.q.p + b * p.q.sb + h * p.q.sh + static_cast<long>(i) * p.q.sn;
-#pragma unroll
-    for (int blk = 0; blk < C::KB; ++blk) {
-      uint32_t w[C::KE / 2];
-      load_words(q + 32 * blk + C::KE * t, have, w);
-#pragma unroll
-      for (int s = 0; s < C::KE / 4; ++s) {
-        qf[blk * (C::KE / 4) + s][u] = w[2 * s];
-        qf[blk * (C::KE / 4) + s][2 + u] = w[2 * s + 1];
-      }
+    for (int k = warp; k < D / 16; k += kStepWarps) {
+      uint32_t* f = reinterpret_cast<uint32_t*>(&sm_q[k][lane]);
+      f[u] = have ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * t) : 0u;
+      f[2 + u] = have ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * t + 8) : 0u;
     }
   }
-  if (warp == 0) {
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) sm_q[k][lane] = make_uint4(qf[k][0], qf[k][1], qf[k][2], qf[k][3]);
-  }
   __syncthreads();
-  const uint16_t* kb = p.k.p + b * p.k.sb + hk * p.k.sh;
-  const uint16_t* vb = p.v.p + b * p.v.sb + hk * p.v.sh;
 
-  float o[C::VB][C::VE][4];
+  float o[D / 8][4];
 #pragma unroll
-  for (int i = 0; i < C::VB; ++i)
+  for (int j = 0; j < D / 8; ++j)
 #pragma unroll
-    for (int j = 0; j < C::VE; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[i][j][k] = 0.f;
+    for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  // this lane's rows in ldmatrix: of K (row of 8 keys, half of a k-step) and of V (row of 16 keys, half of 16 columns)
+  const int rk = (lane >> 4) * 8 + (lane & 7), xk = (lane >> 3 & 1) ^ C::swizzle(rk);
+  const int rv = lane & 15, xv = (lane >> 4) ^ C::swizzle(rv);
 
-  auto compute = [&](const Chunk<D>& c, int key0) {
+  auto compute = [&](uint32_t chunk, int key0) {
     float s[2][4];
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
 #pragma unroll
-    for (int blk = 0; blk < C::KB; ++blk)
-#pragma unroll
-      for (int u = 0; u < C::KE / 4; ++u) {
-        uint32_t q[4];
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
-                     : "r"(smem_u32(&sm_q[blk * (C::KE / 4) + u][lane])));
-#pragma unroll
-        for (int n = 0; n < 2; ++n) mma16816(s[n], q, c.k[n][blk][2 * u], c.k[n][blk][2 * u + 1]);
-      }
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t q[4], kf[4];
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
+                   : "r"(smem_u32(&sm_q[k][lane])));
+      ldmatrix(kf, chunk + 2 * D * rk + 16 * (2 * k ^ xk));
+      mma16816(s[0], q, kf[0], kf[1]);
+      mma16816(s[1], q, kf[2], kf[3]);
+    }
     float mx[2] = {-INFINITY, -INFINITY};
     if (CAP) {
       float top = 0.f;
@@ -209,11 +202,9 @@ __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_k
         l[u] *= f[u];
       }
 #pragma unroll
-      for (int i = 0; i < C::VB; ++i)
+      for (int j = 0; j < D / 8; ++j)
 #pragma unroll
-        for (int j = 0; j < C::VE; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[i][j][k] *= f[k >> 1];
+        for (int k = 0; k < 4; ++k) o[j][k] *= f[k >> 1];
     }
     uint32_t pf[4];
 #pragma unroll
@@ -226,30 +217,25 @@ __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_k
         pf[2 * n + u] = pack_bf16x2(p0, p1);
       }
 #pragma unroll
-    for (int i = 0; i < C::VB; ++i)
-#pragma unroll
-      for (int j = 0; j < C::VE; ++j) {
-        const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-        mma16816(o[i][j], pf, __byte_perm(c.v[0][i][j / 2], c.v[1][i][j / 2], sel),
-                 __byte_perm(c.v[2][i][j / 2], c.v[3][i][j / 2], sel));
-      }
+    for (int j = 0; j < D / 16; ++j) {
+      uint32_t vf[4];
+      ldmatrix_trans(vf, chunk + C::CHUNK_B + 2 * D * rv + 16 * (2 * j ^ xv));
+      mma16816(o[2 * j], pf, vf[0], vf[1]);
+      mma16816(o[2 * j + 1], pf, vf[2], vf[3]);
+    }
   };
-
-  Chunk<D> buf[2];
-  int c = split * per + warp;
-  if (c < c_end) load_chunk<D>(buf[0], p, mask, kb, vb, lo + c * kChunk, hi);
-  for (; c < c_end; c += 2 * kStepWarps) {
-    const int next = c + kStepWarps;
-    if (next < c_end) load_chunk<D>(buf[1], p, mask, kb, vb, lo + next * kChunk, hi);
-    compute(buf[0], lo + c * kChunk);
-    if (next >= c_end) break;
-    if (next + kStepWarps < c_end) load_chunk<D>(buf[0], p, mask, kb, vb, lo + (next + kStepWarps) * kChunk, hi);
-    compute(buf[1], lo + next * kChunk);
+  for (int n = 0; c_beg + n * kStepWarps < c_end; ++n) {
+    copies_wait<C::STAGES - 2>();
+    __syncwarp();              // every lane's copies of chunk n are there, and chunk n - 1 has been read
+    load(n + C::STAGES - 1);
+    compute(ring + n % C::STAGES * 2 * C::CHUNK_B, lo + (c_beg + n * kStepWarps) * kChunk);
   }
+  copies_wait<0>();
+  __syncthreads();             // the join's data go over the rings
 
   // join the warps: row statistics, then the outputs
-  float* sm_ml = sh;
-  float* sm_o = sh + 2 * kStepWarps * rows;
+  float* sm_ml = reinterpret_cast<float*>(sh);
+  float* sm_o = sm_ml + 2 * kStepWarps * rows;
   // a cluster's partial outputs and log2 sums, behind the warps'
   float* sm_part = sm_o + kStepWarps * rows * D;
   float* sm_lse = sm_part + rows * (D + 4);
@@ -265,13 +251,8 @@ __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_k
         sm_ml[2 * (warp * rows + r) + 1] = l[u];
       }
 #pragma unroll
-      for (int i = 0; i < C::VB; ++i)
-#pragma unroll
-        for (int j = 0; j < C::VE; ++j) {
-          float* d = sm_o + (warp * rows + r) * D + 64 * i + j;
-          d[2 * t * C::VE] = o[i][j][2 * u];
-          d[(2 * t + 1) * C::VE] = o[i][j][2 * u + 1];
-        }
+      for (int j = 0; j < D / 8; ++j)
+        *reinterpret_cast<float2*>(sm_o + (warp * rows + r) * D + 8 * j + 2 * t) = make_float2(o[j][2 * u], o[j][2 * u + 1]);
     }
   }
   __syncthreads();
@@ -320,22 +301,27 @@ __global__ void __launch_bounds__(kStepWarps * 32, D == 128 ? 1 : 2) attn_step_k
 }
 
 // Row statistics and outputs of the warps, and of the CTA for its cluster.
-constexpr int step_smem(int rows, int D) { return 4 * rows * (kStepWarps * (D + 2) + D + 5); }
+constexpr int join_smem(int rows, int D) { return 4 * rows * (kStepWarps * (D + 2) + D + 5); }
 
 }  // namespace
+
+int attn_step_ctas(int D) {
+  return D == 128 ? StepCfg<128>::CTAS : D == 64 ? StepCfg<64>::CTAS : D == 32 ? StepCfg<32>::CTAS : StepCfg<16>::CTAS;
+}
 
 cudaError_t launch_attn_step(const AttnParams& p, const AttnSide& q, const AttnSide& k, const AttnSide& v,
                              cudaStream_t s) {
   const StepParams sp{p, q, k, v};
   const dim3 grid(static_cast<unsigned>(static_cast<long>(p.splits) * p.B * p.Hk));
-  const int rows = p.G * p.mask.Nq, smem = step_smem(rows, p.D);
   auto go = [&](auto d, auto cap) {
     constexpr int D = decltype(d)::value;
+    using C = StepCfg<D>;
+    static_assert(join_smem(kAttnStepRows, D) <= C::RING_B, "the join's data fit over the rings");
+    static_assert(C::CTAS * (C::RING_B + 32 * D + 1024) <= 228 * 1024, "shared memory");
     auto* kern = attn_step_kernel<D, decltype(cap)::value>;
-    if (smem > 48 * 1024) {
-      const cudaError_t e = allow_smem<std::pair<StepCfg<D>, decltype(cap)>>(kern, step_smem(kAttnStepRows, D));
-      if (e != cudaSuccess) return e;
-    }
+    constexpr int smem = C::RING_B;
+    const cudaError_t e = allow_smem<std::pair<C, decltype(cap)>>(kern, smem);
+    if (e != cudaSuccess) return e;
     return launch_splits(kern, grid, kStepWarps * 32, smem, s, dim3(p.splits, 1, 1), p.splits, sp);
   };
   auto by_cap = [&](auto d) { return p.cap > 0.f ? go(d, std::true_type{}) : go(d, std::false_type{}); };
