@@ -32,7 +32,6 @@
 // <= 64: KT = 64 and 256 columns let two CTAs share an SM.  Measured on 2 x 16
 // heads x 4096^2, D = 64: plain 231 us (one CTA: 254), capped 303 (two CTAs,
 // which spill: 364), biased 303 (337); D = 128: plain 291, capped 325.
-#include <climits>
 #include <utility>
 
 #include "attn_common.cuh"
@@ -618,75 +617,74 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p) {
 
 // Documents: the start and the end of the run of equal ids each position lies
 // in (the start twice where the id is negative).  A CTA takes 1024 positions:
-// a bit for each that begins a run, then the nearest bit on either side.  The
-// ends of runs that reach into other chunks are searched for in the ids, 1024
-// at a time, where there are few chunks (ONE: one launch).  That is quadratic
-// in the chunks, so with many of them a first launch (SUMS) leaves each chunk's
-// last and first beginning in its first entry, a second turns them into what
-// lies before and behind each chunk, a third (ENDS) does the rest.  One
-// document, one launch (three): 8192 keys 13 us (11), 32768 36 (11), 2^20 1276 (22).
-constexpr int kDocThreads = 256, kDocChunk = 1024, kDocSearched = 8;   // chunks searched in one launch
+// a bit for each that begins a run, then the nearest bit on either side.  Where
+// runs reach into other chunks: with few chunks every CTA makes the bits of
+// them all (ONE: one launch); with many a first launch (SUMS) leaves each
+// chunk's last and first beginning in its first entry, a second turns them into
+// what lies before and behind each chunk, a third (ENDS) does the rest.
+// Latency: 8192 keys 4 us, 32768 8, 2^20 20.
+constexpr int kDocThreads = 1024, kDocChunk = 1024, kDocOne = 16;   // chunks done in one launch
 enum class Doc { ONE, SUMS, ENDS };
 template <Doc HOW>
 __global__ void __launch_bounds__(kDocThreads) attn_documents_kernel(const int32_t* ids, int2* doc, int N, int chunks) {
-  __shared__ uint32_t bits[kDocChunk / 32];
-  __shared__ int left, right;
+  constexpr int WORDS = kDocChunk / 32;
+  __shared__ uint32_t all_bits[HOW == Doc::ONE ? kDocOne * WORDS : WORDS];
+  __shared__ int left, right, before_word[WORDS], behind_word[WORDS];
   const int b = blockIdx.x / chunks, c0 = (blockIdx.x - b * chunks) * kDocChunk;
+  const int from = HOW == Doc::ONE ? 0 : c0, words = HOW == Doc::ONE ? chunks * WORDS : WORDS;
+  uint32_t* bits = all_bits + (c0 - from) / 32;
   ids += static_cast<long>(b) * N;
   doc += static_cast<long>(b) * N;
-  auto begins = [&](int i) { return i <= 0 || i >= N || ids[i] != ids[i - 1]; };   // N begins what is behind
-#pragma unroll
-  for (int k = 0; k < kDocChunk; k += kDocThreads) {
-    const uint32_t w = __ballot_sync(~0u, begins(c0 + k + static_cast<int>(threadIdx.x)));
-    if ((threadIdx.x & 31) == 0) bits[(k + threadIdx.x) / 32] = w;
+  const int t = threadIdx.x, lane = t & 31;
+#pragma unroll 8
+  for (int k = 0; k < 32 * words; k += kDocThreads) {
+    const int i = from + k + t;
+    const int id = i < N ? ids[i] : 0, edge = lane == 0 && i > 0 && i < N ? ids[i - 1] : 0;
+    const int before = __shfl_up_sync(~0u, id, 1);
+    const uint32_t w = __ballot_sync(~0u, i == 0 || i >= N || id != (lane == 0 ? edge : before));   // N begins what is behind
+    if (lane == 0) all_bits[(k + t) / 32] = w;
   }
   if (threadIdx.x == 0) {
     left = HOW == Doc::ENDS ? doc[c0].x : -1;
-    right = HOW == Doc::ENDS ? doc[c0].y : INT_MAX;
+    right = HOW == Doc::ENDS ? doc[c0].y : N;
   }
   __syncthreads();
-  if constexpr (HOW == Doc::SUMS) {
-    if (threadIdx.x < kDocChunk / 32 && bits[threadIdx.x]) {
-      const int at = c0 + 32 * static_cast<int>(threadIdx.x);
-      atomicMax(&left, at + 31 - __clz(bits[threadIdx.x]));
-      atomicMin(&right, at + __ffs(bits[threadIdx.x]) - 1);
+  if constexpr (HOW != Doc::ENDS) {
+    const int mine = (c0 - from) / 32;   // ONE: the words before and behind the chunk; SUMS: its own
+    static_assert(kDocOne * WORDS <= kDocThreads, "a thread a word");
+    if (t < words && all_bits[t]) {
+      if (HOW == Doc::SUMS || t < mine) atomicMax(&left, from + 32 * t + 31 - __clz(all_bits[t]));
+      if (HOW == Doc::SUMS || t >= mine + WORDS) atomicMin(&right, from + 32 * t + __ffs(all_bits[t]) - 1);
     }
     __syncthreads();
-    if (threadIdx.x == 0) doc[c0] = make_int2(left, right);
+    if (HOW == Doc::SUMS && t == 0) doc[c0] = make_int2(left, right);
   }
-  if constexpr (HOW == Doc::ONE) {   // the run that reaches into the chunk from the left, and the one out of it
-    for (int lo = c0; (bits[0] & 1u) == 0 && left < 0;) {
-      lo -= kDocChunk;   // 0 begins a run, so this ends
-      int at = -1;
-      for (int i = lo + static_cast<int>(threadIdx.x); i < lo + kDocChunk; i += kDocThreads)
-        if (i >= 0 && begins(i)) at = i;
-      __syncthreads();   // the loop's test of `left` is done
-      if (at >= 0) atomicMax(&left, at);
-      __syncthreads();
+  if constexpr (HOW != Doc::SUMS) {
+    static_assert(WORDS == 32, "a lane a word");
+    if (t < WORDS) {   // the nearest beginnings before and behind each word
+      int x = bits[t] ? c0 + 32 * t + 31 - __clz(bits[t]) : -1, y = bits[t] ? c0 + 32 * t + __ffs(bits[t]) - 1 : N;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int a = __shfl_up_sync(~0u, x, o), z = __shfl_down_sync(~0u, y, o);
+        if (t >= o) x = max(x, a);
+        if (t + o < 32) y = min(y, z);
+      }
+      x = __shfl_up_sync(~0u, x, 1);
+      y = __shfl_down_sync(~0u, y, 1);
+      before_word[t] = t > 0 ? max(x, left) : left;
+      behind_word[t] = t < 31 ? min(y, right) : right;
     }
-    for (int lo = c0 + kDocChunk; right == INT_MAX; lo += kDocChunk) {
-      int at = INT_MAX;
-      for (int i = lo + kDocChunk - kDocThreads + static_cast<int>(threadIdx.x); i >= lo; i -= kDocThreads)
-        if (begins(i)) at = min(i, N);
-      __syncthreads();
-      if (at != INT_MAX) atomicMin(&right, at);
-      __syncthreads();
-    }
-  }
-  if constexpr (HOW != Doc::SUMS)
-    for (int k = threadIdx.x; k < kDocChunk; k += kDocThreads) {
-      const int i = c0 + k;
+    __syncthreads();
+#pragma unroll
+    for (int k = t; k < kDocChunk; k += kDocThreads) {
+      const int i = c0 + k, w = k / 32;
       if (i >= N) break;
-      int w = k / 32;
-      uint32_t m = bits[w] & (~0u >> (31 - k % 32));          // bits up to k
-      while (m == 0 && w > 0) m = bits[--w];
-      const int start = m ? c0 + 32 * w + 31 - __clz(m) : left;
-      w = k / 32;
-      m = k % 32 == 31 ? 0u : bits[w] & (~0u << (k % 32 + 1));  // bits behind k
-      while (m == 0 && w < kDocChunk / 32 - 1) m = bits[++w];
-      const int end = m ? min(c0 + 32 * w + __ffs(m) - 1, N) : right;
+      const uint32_t m = bits[w] & (~0u >> (31 - lane)), z = lane == 31 ? 0u : bits[w] & (~0u << (lane + 1));
+      const int start = m ? c0 + 32 * w + 31 - __clz(m) : before_word[w];
+      const int end = z ? min(c0 + 32 * w + __ffs(z) - 1, N) : behind_word[w];
       doc[i] = make_int2(start, ids[i] < 0 ? start : end);
     }
+  }
 }
 
 // A batch's chunks: (last, first beginning in the chunk) to (last beginning
@@ -732,7 +730,7 @@ __global__ void __launch_bounds__(kDocJoin) attn_document_ends_kernel(int2* doc,
 cudaError_t launch_attn_documents(const int32_t* ids, int2* doc, int B, int N, cudaStream_t s) {
   const int chunks = (N + kDocChunk - 1) / kDocChunk;
   const unsigned grid = static_cast<unsigned>(static_cast<long>(B) * chunks);
-  if (chunks <= kDocSearched) {
+  if (chunks <= kDocOne) {
     attn_documents_kernel<Doc::ONE><<<grid, kDocThreads, 0, s>>>(ids, doc, N, chunks);
   } else {
     attn_documents_kernel<Doc::SUMS><<<grid, kDocThreads, 0, s>>>(ids, doc, N, chunks);

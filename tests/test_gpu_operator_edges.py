@@ -50,8 +50,8 @@ def test_slopes_of_any_sign(slope):
 
 
 @pytest.mark.parametrize("N,cuts,dead", [
-    (8 * 1024, (), ()), (8 * 1024, (1024, 7 * 1024), (1,)),                        # searched in one launch
-    (9 * 1024, (), ()), (33 * 1024, (5, 1023, 1024, 20000, 32767, 32768), (4,)),  # in three
+    (16 * 1024, (), ()), (16 * 1024, (1024, 15 * 1024), (1,)),                        # one launch
+    (17 * 1024, (), ()), (33 * 1024, (5, 1023, 1024, 20000, 32767, 32768), (4,)),  # in three
     (40001, (40000,), ()), (70000, (1, 2, 3, 65535, 65536, 65537, 69999), (1, 6))])
 def test_documents_of_long_sequences(N, cuts, dead):
     g = torch.Generator(device=DEV).manual_seed(23)
