@@ -12,6 +12,10 @@
 // Rows keep a running reference and sum as in the tiled kernel.  The keys are
 // split over CTAs, within a CTA over its warps, which join in shared memory;
 // up to eight splits are a cluster and join there too.
+//
+// D = 128, 16 ragged caches of up to 32768 keys, 8 key heads of 4 query heads:
+// 211 us, 6.4 TB/s (with the chunks in registers, one CTA of 8 warps an SM, 238
+// to 254); 64 caches of 1024: 43 us (96).
 #include <type_traits>
 #include <utility>
 

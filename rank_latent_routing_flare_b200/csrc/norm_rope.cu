@@ -21,6 +21,12 @@
 // 10^6 and more keep their angles; sine and cosine in fp32).
 // Sums and products are fp32, in paired instructions; results are rounded to
 // bf16 once, at the store.
+//
+// Measured: keys of 8 heads of 16, 2^20 points in space, 121 us (4.5 TB/s); 32 x
+// 4096 tokens, 8 + 8 heads of 32, padded, 52 us (4.2); backward of 32 + 8 heads
+// of 128, 2 x 8191 tokens, 132 us (3.8), of 8 + 8 heads of 16, 4 x 65536 points, 96
+// us (4.2).  The same accesses without arithmetic take 95, 47, 93 and 78 us: short
+// rows and two strides keep them from the 6.5 TB/s of a plain copy.
 #include <algorithm>
 
 #include "flare_internal.h"

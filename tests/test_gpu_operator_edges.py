@@ -176,3 +176,31 @@ def test_preparation_of_many_heads_and_single_rows():
         assert torch.equal(one, y[:, h:h + 1])
     last, _ = fl.flare_qk_norm_rope_fwd(x[:, 7:8, 4:5], None, gains[7].clone(), freqs=freqs, positions=i32(4).view(1, 1))
     assert torch.equal(last, y[:, 7:8, 4:5])
+
+
+def test_offsets_beyond_32_bits():
+    """Batch entries 2^31 elements apart, in every tensor that takes strides."""
+    far, N, D = 1 << 31, 150, 32
+    whole = torch.empty(far + 4 * N * D, dtype=torch.bfloat16, device=DEV)
+
+    def rows(n):   # the n-th tensor of two batch entries and one head
+        return whole.as_strided((2, 1, N, D), (far, N * D, D, 1), n * N * D)
+
+    Q, K, V, dY, _ = make(2, 1, 1, N, N, D, seed=30)
+    want = fl.flare_attention_fwd_train(Q, K, V, causal=True)
+    grads = fl.flare_attention_bwd(Q, K, V, *want, dY, causal=True)
+    for n, t in enumerate((Q, K, V)):
+        rows(n).copy_(t)
+    Y, L = fl.flare_attention_fwd_train(rows(0), rows(1), rows(2), Y=rows(3), causal=True)
+    assert torch.equal(Y, want[0]) and torch.equal(L, want[1])
+    step = fl.flare_attention_fwd(rows(0)[:, :, -1:], rows(1), rows(2), causal=True)
+    assert torch.equal(step, fl.flare_attention_fwd(Q[:, :, -1:], K, V, causal=True))
+    got = fl.flare_attention_bwd(rows(0), rows(1), rows(2), Y, L, dY, causal=True, dV=rows(3))
+    assert all(torch.equal(a, b) for a, b in zip(got, grads))
+    freqs = 100.0 ** (-torch.arange(D // 2, device=DEV) / (D // 2))
+    Qr, Kr = fl.flare_qk_norm_rope_fwd(Q, K, freqs=freqs)
+    got = fl.flare_qk_norm_rope_fwd(rows(0), rows(1), freqs=freqs, Qr=rows(2), Kr=rows(3))
+    assert torch.equal(got[0], Qr) and torch.equal(got[1], Kr)
+    back = fl.flare_qk_norm_rope_bwd(Q, K, Qr, Kr, freqs=freqs)
+    got = fl.flare_qk_norm_rope_bwd(rows(0), rows(1), rows(2), rows(3), freqs=freqs)
+    assert torch.equal(got["dQ"], back["dQ"]) and torch.equal(got["dK"], back["dK"])
