@@ -42,14 +42,14 @@ AttnPlan make_attn_plan(int64_t B, int64_t Hq, int64_t Hk, int64_t Nq, int64_t N
   AttnPlan pl{};
   pl.step = Hq / Hk * Nq <= kAttnStepRows;
   if (pl.step) {
-    // CTAs for three waves: few enough that their beginnings and ends do not
-    // show, many enough that ragged caches even out; up to five while a split
-    // has 2048 keys.  With two (four) waves, D = 128, 8 key heads: 16 ragged
-    // caches of 8192 keys 81 us (80; three 78), of 32768 250 (218; five 213), 64 of
-    // 1024 40 (49; three 43).  Eight splits join in their cluster; more, in a
-    // launch of 5 us, have 512 keys each.
+    // CTAs for two waves: few enough that their beginnings and ends do not
+    // show, many enough that ragged caches even out; up to four while a split
+    // has 2048 keys.  With two (three, four) waves, D = 128, 8 key heads: 64 ragged
+    // caches of 1024 keys 31 us (34, 38), 16 of 8192 63 (64, 64), 16 of 32768 203
+    // (198, 194).  Eight splits join in their cluster; more, in a launch of 5 us,
+    // have 512 keys each.
     const int64_t wave = kNumSM * attn_step_ctas(static_cast<int>(D)), heads = B * Hk;
-    const int64_t want = std::max(3 * wave / heads, std::min(5 * wave / heads, Nk / 2048));
+    const int64_t want = std::max(2 * wave / heads, std::min(4 * wave / heads, Nk / 2048));
     const int64_t most = std::max(std::min<int64_t>(Nk / 128, kAttnClusterSplits), Nk / 512);
     pl.splits = static_cast<int>(std::max<int64_t>(1, std::min({want, most, int64_t(256)})));
   } else {

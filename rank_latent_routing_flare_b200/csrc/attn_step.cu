@@ -1,23 +1,27 @@
 // Exact softmax attention of few query rows: single new tokens over a long
 // cache.  A key head's query rows (its G query heads times Nq <= 16 rows)
 // share every key and value, so K and V are read once and the kernel is bound
-// by HBM; the products (m16n8k16 mma.sync, 16 rows at a time) are far below
-// the tensor pipe's rate.
+// by HBM.  The products are mma.sync m16n8k16 with the rows as columns, eight
+// (NT = 1) or sixteen (NT = 2) of them: S^T = K Q^T, O^T += V^T P^T, far below the
+// tensor pipe's rate, and little else to issue per key.
 //
 // Each warp streams chunks of 16 keys through a ring of its own in shared
 // memory (16-byte cp.async, rows swizzled so that ldmatrix meets no bank
 // conflict): what is in flight takes no registers, so that several CTAs of
 // four warps share an SM and one's beginning and end run under the others'
-// loads.  K's fragments come from ldmatrix, V's from its transposing form.
-// Rows keep a running reference and sum as in the tiled kernel.  The keys are
-// split over CTAs, within a CTA over its warps, which join in shared memory;
-// up to eight splits are a cluster and join there too.
+// loads.  K's fragments come from ldmatrix, V's from its transposing form; the
+// weights turn from a sum's layout into an operand's by movmatrix.  Rows keep a
+// running reference and sum as in the tiled kernel.  The keys are split over
+// CTAs, within a CTA over its warps, which join in shared memory; up to eight
+// splits are a cluster and join there too.
 //
-// D = 128, 16 ragged caches of up to 32768 keys, 8 key heads of 4 query heads:
-// 211 us, 6.4 TB/s (with the chunks in registers, one CTA of 8 warps an SM, 238
-// to 254); 64 caches of 1024: 43 us (96).
+// D = 128, 8 key heads of 4 query heads, ragged caches: 16 of up to 32768 keys 194
+// us with the join, 6.9 TB/s; 64 of up to 1024 31 us, 5.1.  (Chunks in
+// registers, one CTA of 8 warps an SM, rows as the products' 16 rows: 258 and 96.
+// As here but for the rows: 216 and 43, half of the issue slots taken.)
+#include <climits>
+#include <tuple>
 #include <type_traits>
-#include <utility>
 
 #include "attn_common.cuh"
 #include "ops_internal.h"
@@ -43,6 +47,9 @@ struct StepCfg {
   __device__ static constexpr int swizzle(int r) { return U >= 8 ? r & 7 : U == 4 ? r >> 1 & 3 : r >> 2 & 1; }
 };
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {   // zeros if not ok
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
@@ -63,32 +70,52 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// 8 x 8 values, row g of lanes (g, 0 .. 3), to column g.
+__device__ __forceinline__ uint32_t transposed(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+
 // Copies of a chunk's rows of K and V, zeros from key `end` on.
 template <int D>
 __device__ __forceinline__ void load_chunk(uint32_t dst, const StepParams& p, const BatchMask& m, const uint16_t* kb,
                                            const uint16_t* vb, int key0, int end) {
   using C = StepCfg<D>;
-  const int lane = threadIdx.x & 31;
+  constexpr int ROWS = 32 / C::U, N = kChunk / ROWS;   // rows a warp copies at once
+  const int lane = threadIdx.x & 31, r0 = lane / C::U, u = lane % C::U;
+  const uint32_t at0 = 2 * D * r0 + 16 * (u ^ C::swizzle(r0));
+  auto at = [&](int i) { return dst + (at0 ^ 16 * C::swizzle(i * ROWS)) + 2 * D * ROWS * i; };
+  const uint16_t *k = kb + static_cast<long>(key0 + r0) * p.k.sn + 8 * u, *v = vb + static_cast<long>(key0 + r0) * p.v.sn + 8 * u;
+  if (key0 + kChunk <= end && !m.doc) {
 #pragma unroll
-  for (int i = 0; i < kChunk * C::U / 32; ++i) {
-    const int e = lane + 32 * i, r = e / C::U, u = e % C::U, key = key0 + r;
-    const uint32_t at = dst + 2 * D * r + 16 * (u ^ C::swizzle(r));
-    const bool ok = key < end;
-    copy16(at, ok ? kb + static_cast<long>(key) * p.k.sn + 8 * u : kb, ok);
-    bool okv = ok;
+    for (int i = 0; i < N; ++i) {
+      copy16(at(i), k);
+      copy16(at(i) + C::CHUNK_B, v);
+      k += ROWS * p.k.sn;
+      v += ROWS * p.v.sn;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int key = key0 + r0 + i * ROWS;
+    bool ok = key < end;
+    copy16(at(i), ok ? k + i * ROWS * p.k.sn : kb, ok);
     if (m.doc && ok) {   // a weight of 0 does not erase a NaN: padding inside the range is not read
       const int2 d = m.doc[key];
-      okv = d.x != d.y;
+      ok = d.x != d.y;
     }
-    copy16(at + C::CHUNK_B, okv ? vb + static_cast<long>(key) * p.v.sn + 8 * u : vb, okv);
+    copy16(at(i) + C::CHUNK_B, ok ? v + i * ROWS * p.v.sn : vb, ok);
   }
 }
 
 // CAP: capped scores; without, the tanh's coefficients take no registers.
-template <int D, bool CAP>
+template <int D, bool CAP, int NT>
 __global__ void __launch_bounds__(kStepWarps * 32, StepCfg<D>::CTAS) attn_step_kernel(const StepParams p) {
   using C = StepCfg<D>;
-  extern __shared__ __align__(128) uint8_t sh[];   // the warps' rings; behind the loop the join's data
+  extern __shared__ uint8_t sh_raw[];   // the warps' rings; behind the loop the join's data
+  uint8_t* sh = sh_raw + (256 - smem_u32(sh_raw) % 256) % 256;   // rows on multiples of their size
   const AttnParams& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int split = blockIdx.x % a.splits, bk = blockIdx.x / a.splits, b = bk / a.Hk, hk = bk % a.Hk;
@@ -119,113 +146,153 @@ __global__ void __launch_bounds__(kStepWarps * 32, StepCfg<D>::CTAS) attn_step_k
 #pragma unroll
   for (int n = 0; n < C::STAGES - 1; ++n) load(n);
 
-  // this lane's two rows: r = i G + head
-  int2 iv[2];
-  int pos[2];
-  float slope2[2];
-  __shared__ uint4 sm_q[D / 16][32];   // Q's operand fragments, the same for every warp: read per chunk, they hold no registers
+  // this lane's rows 8 v + 2 t + u: r = i G + head
+  int2 iv[NT][2];
+  int pos[NT][2];
+  float slope2[NT][2];
+  int all_lo = 0, all_hi = INT_MAX;   // keys that every row sees
+  __shared__ uint2 sm_q[D / 16][NT][32];   // Q's operand fragments, the same for every warp: read per chunk, they hold no registers
   const ScoreOps ops(a.scale, a.cap, true);
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int r = g + 8 * u, i = r / a.G, h = hk * a.G + r % a.G;
-    const bool have = r < rows;
-    iv[u] = have ? row_interval(mask, i) : make_int2(0, 0);
-    pos[u] = bias_position(mask, have ? i : 0, iv[u]);
-    slope2[u] = have && a.slopes ? a.slopes[h] * kLog2e : 0.f;
-    const uint16_t* q = p.q.p + b * p.q.sb + h * p.q.sh + static_cast<long>(i) * p.q.sn;
-    for (int k = warp; k < D / 16; k += kStepWarps) {
-      uint32_t* f = reinterpret_cast<uint32_t*>(&sm_q[k][lane]);
-      f[u] = have ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * t) : 0u;
-      f[2 + u] = have ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * t + 8) : 0u;
+  for (int v = 0; v < NT; ++v) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = 8 * v + 2 * t + u, i = r / a.G, h = hk * a.G + r % a.G;
+      const bool have = r < rows;
+      iv[v][u] = have ? row_interval(mask, i) : make_int2(0, INT_MAX);   // (what is no row may see anything)
+      pos[v][u] = bias_position(mask, have ? i : 0, iv[v][u]);
+      slope2[v][u] = have && a.slopes ? a.slopes[h] * kLog2e : 0.f;
+      all_lo = max(all_lo, iv[v][u].x);
+      all_hi = min(all_hi, iv[v][u].y);
     }
+    const int r = 8 * v + g, i = r / a.G, h = hk * a.G + r % a.G;
+    const uint16_t* q = p.q.p + b * p.q.sb + h * p.q.sh + static_cast<long>(i) * p.q.sn + 2 * t;
+    for (int k = warp; k < D / 16; k += kStepWarps)
+      sm_q[k][v][lane] = r < rows ? make_uint2(*reinterpret_cast<const uint32_t*>(q + 16 * k),
+                                               *reinterpret_cast<const uint32_t*>(q + 16 * k + 8))
+                                  : make_uint2(0u, 0u);
+  }
+#pragma unroll
+  for (int x = 1; x < 4; x *= 2) {
+    all_lo = max(all_lo, __shfl_xor_sync(~0u, all_lo, x));
+    all_hi = min(all_hi, __shfl_xor_sync(~0u, all_hi, x));
   }
   __syncthreads();
 
-  float o[D / 8][4];
+  float o[D / 16][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
-  for (int j = 0; j < D / 8; ++j)
+  for (int v = 0; v < NT; ++v) {
+    m[v][0] = m[v][1] = -INFINITY;
+    l[v][0] = l[v][1] = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  // this lane's rows in ldmatrix: of K (row of 8 keys, half of a k-step) and of V (row of 16 keys, half of 16 columns)
-  const int rk = (lane >> 4) * 8 + (lane & 7), xk = (lane >> 3 & 1) ^ C::swizzle(rk);
-  const int rv = lane & 15, xv = (lane >> 4) ^ C::swizzle(rv);
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[j][v][k] = 0.f;
+  }
+  // where this lane's rows lie in ldmatrix: keys 0-7, 8-15 by the first (K) or the second (V) half of 16 columns, and so on
+  const int rk = lane & 15, rv = (lane >> 4) * 8 + (lane & 7);
+  const uint32_t at_k = 2 * D * rk + 16 * ((lane >> 4) ^ C::swizzle(rk));
+  const uint32_t at_v = C::CHUNK_B + 2 * D * rv + 16 * ((lane >> 3 & 1) ^ C::swizzle(rv));
 
   auto compute = [&](uint32_t chunk, int key0) {
-    float s[2][4];
+    float s[NT][4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int v = 0; v < NT; ++v)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
+      for (int k = 0; k < 4; ++k) s[v][k] = 0.f;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      uint32_t q[4], kf[4];
-      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
-                   : "r"(smem_u32(&sm_q[k][lane])));
-      ldmatrix(kf, chunk + 2 * D * rk + 16 * (2 * k ^ xk));
-      mma16816(s[0], q, kf[0], kf[1]);
-      mma16816(s[1], q, kf[2], kf[3]);
+      uint32_t kf[4];
+      ldmatrix(kf, (chunk + at_k) ^ 32 * k);
+#pragma unroll
+      for (int v = 0; v < NT; ++v) {
+        uint32_t q[2];
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(q[0]), "=r"(q[1]) : "r"(smem_u32(&sm_q[k][v][lane])));
+        mma16816(s[v], kf, q[0], q[1]);
+      }
     }
-    float mx[2] = {-INFINITY, -INFINITY};
     if (CAP) {
       float top = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(s[0][k]), fabsf(s[1][k])));
-      if (__all_sync(~0u, ops.small(top))) {
+      for (int v = 0; v < NT; ++v)
 #pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-          float* x = &s[k / 4][k % 4];
-          f2_unpack(ops.poly(f2_pack(x[0], x[1]), f2_dup(0.f)), x[0], x[1]);
+        for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(s[v][k]));
+      const bool small = __all_sync(~0u, ops.small(top));
+#pragma unroll
+      for (int v = 0; v < NT; ++v) {
+        if (small) {
+          f2_unpack(ops.poly(f2_pack(s[v][0], s[v][1]), f2_dup(0.f)), s[v][0], s[v][1]);
+          f2_unpack(ops.poly(f2_pack(s[v][2], s[v][3]), f2_dup(0.f)), s[v][2], s[v][3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[v][k] = ops.capped(s[v][k]);
         }
-      } else {
+      }
+    } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s[k / 4][k % 4] = ops.capped(s[k / 4][k % 4]);
+      for (int v = 0; v < NT; ++v)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[v][k] *= ops.c2;
+    }
+    if (a.slopes) {
+#pragma unroll
+      for (int v = 0; v < NT; ++v)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          s[v][k] = fmaf(-slope2[v][k & 1], fabsf(static_cast<float>(pos[v][k & 1] - (key0 + g + 8 * (k >> 1)))), s[v][k]);
+    }
+    if (key0 < all_lo || key0 + kChunk > all_hi) {
+#pragma unroll
+      for (int v = 0; v < NT; ++v)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = key0 + g + 8 * (k >> 1);
+          if (key < iv[v][k & 1].x || key >= iv[v][k & 1].y) s[v][k] = -INFINITY;
+        }
+    }
+    bool grown = false;
+#pragma unroll
+    for (int v = 0; v < NT; ++v)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) grown |= fmaxf(s[v][u], s[v][2 + u]) > m[v][u] + 8.f;
+    if (__any_sync(~0u, grown)) {
+#pragma unroll
+      for (int v = 0; v < NT; ++v) {
+        float f[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float mx = fmaxf(s[v][u], s[v][2 + u]);
+#pragma unroll
+          for (int x = 4; x < 32; x *= 2) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, x));
+          const float m_new = fmaxf(m[v][u], mx);
+          f[u] = m[v][u] == -INFINITY ? 0.f : ex2_mufu(m[v][u] - m_new);
+          m[v][u] = m_new;
+          l[v][u] *= f[u];
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[j][v][k] *= f[k & 1];
       }
     }
+    uint32_t pf[NT][2];
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int v = 0; v < NT; ++v) {
+      const float b0 = m[v][0] == -INFINITY ? 0.f : m[v][0], b1 = m[v][1] == -INFINITY ? 0.f : m[v][1];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int u = k >> 1, key = key0 + 8 * n + 2 * t + (k & 1);
-        float x = CAP ? s[n][k] : s[n][k] * ops.c2;
-        if (a.slopes) x = fmaf(-slope2[u], fabsf(static_cast<float>(pos[u] - key)), x);
-        if (key < iv[u].x || key >= iv[u].y) x = -INFINITY;
-        s[n][k] = x;
-        mx[u] = fmaxf(mx[u], x);
+      for (int n = 0; n < 2; ++n) {
+        const float p0 = ex2_mufu(s[v][2 * n] - b0), p1 = ex2_mufu(s[v][2 * n + 1] - b1);
+        l[v][0] += p0;
+        l[v][1] += p1;
+        pf[v][n] = transposed(pack_bf16x2(p0, p1));
       }
-    if (__any_sync(~0u, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
-      float f[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        mx[u] = fmaxf(mx[u], __shfl_xor_sync(~0u, mx[u], 1));
-        mx[u] = fmaxf(mx[u], __shfl_xor_sync(~0u, mx[u], 2));
-        const float m_new = fmaxf(m[u], mx[u]);
-        f[u] = m[u] == -INFINITY ? 0.f : ex2_mufu(m[u] - m_new);
-        m[u] = m_new;
-        l[u] *= f[u];
-      }
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[j][k] *= f[k >> 1];
     }
-    uint32_t pf[4];
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float base = m[u] == -INFINITY ? 0.f : m[u];
-        const float p0 = ex2_mufu(s[n][2 * u] - base), p1 = ex2_mufu(s[n][2 * u + 1] - base);
-        l[u] += p0 + p1;
-        pf[2 * n + u] = pack_bf16x2(p0, p1);
-      }
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
       uint32_t vf[4];
-      ldmatrix_trans(vf, chunk + C::CHUNK_B + 2 * D * rv + 16 * (2 * j ^ xv));
-      mma16816(o[2 * j], pf, vf[0], vf[1]);
-      mma16816(o[2 * j + 1], pf, vf[2], vf[3]);
+      ldmatrix_trans(vf, (chunk + at_v) ^ 32 * j);
+#pragma unroll
+      for (int v = 0; v < NT; ++v) mma16816(o[j][v], vf, pf[v][0], pf[v][1]);
     }
   };
   for (int n = 0; c_beg + n * kStepWarps < c_end; ++n) {
@@ -245,20 +312,25 @@ __global__ void __launch_bounds__(kStepWarps * 32, StepCfg<D>::CTAS) attn_step_k
   float* sm_lse = sm_part + rows * (D + 4);
   const bool in_cluster = a.splits > 1 && a.splits <= kAttnClusterSplits;
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    l[u] += __shfl_xor_sync(~0u, l[u], 1);
-    l[u] += __shfl_xor_sync(~0u, l[u], 2);
-    const int r = g + 8 * u;
-    if (r < rows) {
-      if (t == 0) {
-        sm_ml[2 * (warp * rows + r)] = m[u];
-        sm_ml[2 * (warp * rows + r) + 1] = l[u];
-      }
+  for (int v = 0; v < NT; ++v)
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-        *reinterpret_cast<float2*>(sm_o + (warp * rows + r) * D + 8 * j + 2 * t) = make_float2(o[j][2 * u], o[j][2 * u + 1]);
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int x = 4; x < 32; x *= 2) l[v][u] += __shfl_xor_sync(~0u, l[v][u], x);
+      const int r = 8 * v + 2 * t + u;
+      if (r < rows) {
+        if (g == 0) {
+          sm_ml[2 * (warp * rows + r)] = m[v][u];
+          sm_ml[2 * (warp * rows + r) + 1] = l[v][u];
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          float* d = sm_o + (warp * rows + r) * D + 16 * j + g;
+          d[0] = o[j][v][u];
+          d[8] = o[j][v][2 + u];
+        }
+      }
     }
-  }
   __syncthreads();
   for (int idx = threadIdx.x; idx < rows * (D / 2); idx += blockDim.x) {
     const int r = idx / (D / 2), d = 2 * (idx % (D / 2));
@@ -317,18 +389,21 @@ cudaError_t launch_attn_step(const AttnParams& p, const AttnSide& q, const AttnS
                              cudaStream_t s) {
   const StepParams sp{p, q, k, v};
   const dim3 grid(static_cast<unsigned>(static_cast<long>(p.splits) * p.B * p.Hk));
-  auto go = [&](auto d, auto cap) {
+  auto go = [&](auto d, auto cap, auto nt) {
     constexpr int D = decltype(d)::value;
     using C = StepCfg<D>;
     static_assert(join_smem(kAttnStepRows, D) <= C::RING_B, "the join's data fit over the rings");
-    static_assert(C::CTAS * (C::RING_B + 32 * D + 1024) <= 228 * 1024, "shared memory");
-    auto* kern = attn_step_kernel<D, decltype(cap)::value>;
-    constexpr int smem = C::RING_B;
-    const cudaError_t e = allow_smem<std::pair<C, decltype(cap)>>(kern, smem);
+    static_assert(C::CTAS * (C::RING_B + 256 + 32 * D + 1024) <= 228 * 1024, "shared memory");
+    auto* kern = attn_step_kernel<D, decltype(cap)::value, decltype(nt)::value>;
+    constexpr int smem = C::RING_B + 256;
+    const cudaError_t e = allow_smem<std::tuple<C, decltype(cap), decltype(nt)>>(kern, smem);
     if (e != cudaSuccess) return e;
     return launch_splits(kern, grid, kStepWarps * 32, smem, s, dim3(p.splits, 1, 1), p.splits, sp);
   };
-  auto by_cap = [&](auto d) { return p.cap > 0.f ? go(d, std::true_type{}) : go(d, std::false_type{}); };
+  auto by_rows = [&](auto d, auto cap) {
+    return p.G * p.mask.Nq <= 8 ? go(d, cap, std::integral_constant<int, 1>{}) : go(d, cap, std::integral_constant<int, 2>{});
+  };
+  auto by_cap = [&](auto d) { return p.cap > 0.f ? by_rows(d, std::true_type{}) : by_rows(d, std::false_type{}); };
   switch (p.D) {
     case 16: return by_cap(std::integral_constant<int, 16>{});
     case 32: return by_cap(std::integral_constant<int, 32>{});
