@@ -10,8 +10,10 @@
  *     elements: a head-major tensor has strides (H N D, N D, D), a slice of a
  *     token-major projection [B][N][Ht D] has (N Ht D, D, Ht D).  Every row
  *     starts on a 16-byte boundary (pointers aligned, strides multiples of 8
- *     elements).  The stride of a size-one dimension is not read.  Outputs
- *     must not overlap each other or the inputs.
+ *     elements, at most 2^38).  The stride of a size-one dimension is not read.
+ *     A zero stride (an expanded tensor) is taken for inputs of the
+ *     preparation and for Y, and refused elsewhere.  Outputs must not overlap
+ *     each other or the inputs.
  *   - D in {16, 32, 64, 128}.
  *   - Arguments come in one struct whose members are all 8 bytes wide.
  *     Pointers marked optional may be NULL.
@@ -103,7 +105,18 @@ FLARE_API flare_status flare_qk_norm_rope_bwd(const flare_qk_norm_rope_args* arg
  * Y_i = 0, L_i = -inf and zero gradients, and contributes none.
  *
  * Keys that no row may see (j >= lengths[b], ids below zero) and rows i >=
- * q_lengths[b] may hold anything, infinities and NaN included.
+ * q_lengths[b] may hold anything, infinities and NaN included.  A NaN or an
+ * infinity in a V row that some row of the head sees may also reach rows that
+ * mask it (0 times it is NaN, as in softmax(s) V).
+ *
+ * The cap is 0 or lies in [1e-6, 1e9]; Nq and Nk are at most 2^27.  Products
+ * of bf16 rows, exponentials, sums and statistics are fp32; weights and dS
+ * enter their products in bf16.  Gradients with respect to the slopes are not
+ * computed.
+ *
+ * Workspaces hold an error word in front (flare_last_device_status), the
+ * documents' intervals, the partial results of splits along the keys, or the
+ * backward's row statistics.  Contents are not kept from call to call.
  */
 typedef struct {
   int64_t B, Hq, Hk, Nq, Nk, D;

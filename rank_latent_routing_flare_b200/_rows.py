@@ -14,7 +14,7 @@ from . import _binding as b
 
 ROW_WIDTHS = (16, 32, 64, 128)
 NO_ROWS = (0, 0, 0, 0)
-_bf16 = torch.bfloat16
+_bf16, _dense, empty_like = torch.bfloat16, torch.contiguous_format, torch.empty_like
 
 
 def rows(t):
@@ -88,10 +88,11 @@ def call(name, where, dev, stream, *args):
         raise b.FlareError(st, where)
 
 
-def empty(stream, *args, **kwargs):
-    """torch.empty whose memory is not handed out again before the work on
-    `stream` (None: the current one) that was enqueued by then is done."""
-    t = torch.empty(*args, **kwargs)
+# Memory that a call allocates for work on another stream than the current one
+# is recorded there, so that it is not handed out again before that work is done.
+
+def new_like(like, stream):
+    t = empty_like(like, memory_format=_dense)
     if stream is not None:
         t.record_stream(stream)
     return t
@@ -100,16 +101,21 @@ def empty(stream, *args, **kwargs):
 def output(name, t, like, dev, stream, check):
     """An output of `like`'s shape, new unless given, and its pointer and strides."""
     if t is None:
-        t = empty(stream, like.shape, dtype=_bf16, device=like.device)
+        t = empty_like(like, memory_format=_dense)
+        if stream is not None:
+            t.record_stream(stream)
     elif check:
         return t, check_rows(name, t, like.shape, dev, output=True)
-    return t, rows(t)
+    return (t, (t.data_ptr(), *t.stride()[:3]))
 
 
 def workspace(ws, nbytes, like, stream):
     """The caller's workspace, checked, or a new one."""
     if ws is None:
-        return empty(stream, nbytes if nbytes > 256 else 256, dtype=torch.uint8, device=like.device)
+        ws = torch.empty(nbytes if nbytes > 256 else 256, dtype=torch.uint8, device=like.device)
+        if stream is not None:
+            ws.record_stream(stream)
+        return ws
     check_small("workspace", ws, torch.uint8, None, like.get_device())
     if ws.numel() < nbytes:
         raise ValueError(f"workspace has {ws.numel()} bytes, needs {nbytes}")

@@ -15,7 +15,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _binding as b
-from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, empty, entry, output as _output, ptr, rows,
+from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, entry, output as _output, ptr, rows,
                     workspace as _ws)
 
 # flare_attention_args
@@ -104,7 +104,11 @@ def flare_attention_fwd_train(Q, K, V, lengths=None, q_lengths=None, q_offsets=N
                               slopes=None, causal: bool = False, scale: float = 0.0, cap: float = 0.0, Y=None,
                               L_out=None, workspace=None, stream=None, check: bool = True, device_check: bool = False):
     """flare_attention_fwd that returns (Y, L), what flare_attention_bwd takes."""
-    L = empty(stream, Q.shape[:3], dtype=torch.float32, device=Q.device) if L_out is None else L_out
+    L = L_out
+    if L is None:
+        L = torch.empty(Q.shape[:3], dtype=_f32, device=Q.device)
+        if stream is not None:
+            L.record_stream(stream)
     Y = _forward("flare_attention_fwd_train", Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes,
                  causal, scale, cap, Y, L, workspace, stream, check, device_check)
     return Y, L

@@ -15,7 +15,7 @@ import struct
 import torch
 from torch.autograd.function import once_differentiable
 
-from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, empty, entry, output as _output, ptr, rows,
+from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, entry, new_like, output as _output, ptr, rows,
                     workspace as _ws)
 
 # flare_qk_norm_rope_args
@@ -135,7 +135,7 @@ def flare_qk_norm_rope_bwd(Q=None, K=None, dQr=None, dKr=None, q_gain=None, k_ga
         if gain is None:
             g[name] = None
         elif g.get(name) is None:
-            g[name] = empty(stream, gain.shape, dtype=_f32, device=gain.device)
+            g[name] = new_like(gain, stream)
         elif check:
             check_small(name, g[name], _f32, gain.shape, dev)
     ws, nbytes = 0, 0
