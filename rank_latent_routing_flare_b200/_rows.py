@@ -39,9 +39,7 @@ def check_rows(name, t, shape, dev, output=False):
 
 
 def check_small(name, t, dtype, shape, dev) -> int:
-    """Checks an optional contiguous tensor on GPU `dev` (shape None: any); returns its pointer."""
-    if t is None:
-        return 0
+    """Checks a contiguous tensor on GPU `dev` (shape None: any); returns its pointer."""
     if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or (
             shape is not None and t.shape != shape):
         _refuse(name, t, dtype, shape, dev)

@@ -21,6 +21,7 @@ from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, entry, o
 # flare_attention_args
 _ARGS = struct.Struct("=7q2d12q6q4qq4q12q")
 _f32, _i32 = torch.float32, torch.int32
+_NO_BACKWARD = NO_ROWS * 4
 
 
 @functools.lru_cache(maxsize=4096)
@@ -45,10 +46,12 @@ def _head(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, cau
         q = check_rows("Q", Q, (B, Hq, Nq, D), dev)
         k = check_rows("K", K, (B, Hk, Nk, D), dev)
         v = check_rows("V", V, (B, Hk, Nk, D), dev)
-        small = (check_small("lengths", lengths, _i32, (B,), dev), check_small("q_lengths", q_lengths, _i32, (B,), dev),
-                 check_small("q_offsets", q_offsets, _i32, (B,), dev),
-                 check_small("documents", documents, _i32, (B, Nk), dev),
-                 check_small("prefix", prefix, _i32, (B,), dev), check_small("slopes", slopes, _f32, (Hq,), dev))
+        small = (0 if lengths is None else check_small("lengths", lengths, _i32, (B,), dev),
+                 0 if q_lengths is None else check_small("q_lengths", q_lengths, _i32, (B,), dev),
+                 0 if q_offsets is None else check_small("q_offsets", q_offsets, _i32, (B,), dev),
+                 0 if documents is None else check_small("documents", documents, _i32, (B, Nk), dev),
+                 0 if prefix is None else check_small("prefix", prefix, _i32, (B,), dev),
+                 0 if slopes is None else check_small("slopes", slopes, _f32, (Hq,), dev))
         if prefix is not None and not causal:
             raise ValueError("prefix goes with causal=True")
     else:
@@ -57,25 +60,10 @@ def _head(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, cau
     return (B, Hq, Hk, Nq, Nk, D, bool(causal), scale, cap, *q, *k, *v, *small), (B, Hq, Hk, Nq, Nk, D), dev
 
 
-def _device_check(device_check, ws, stream, where):
-    if device_check:
-        st = b.flare_last_device_status(ws, stream)
-        if st != 0:
-            raise b.FlareError(st, where + " (device status)")
-
-
-def _forward(where, Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap, Y, L,
-             workspace, stream, check, device_check):
-    head, sizes, dev = _head(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap,
-                             check)
-    Y, y = _output("Y", Y, Q, dev, stream, check)
-    if check:
-        check_small("L", L, _f32, Q.shape[:3], dev)
-    ws = _ws(workspace, flare_attention_workspace_bytes(*sizes), Q, stream)
-    args = _ARGS.pack(*head, *y, ptr(L), *NO_ROWS, *NO_ROWS, *NO_ROWS, *NO_ROWS)
-    call("flare_attention_fwd", where, dev, stream, args, ws.data_ptr(), ws.numel())
-    _device_check(device_check, ws, stream, where)
-    return Y
+def _device_check(ws, stream, where):
+    st = b.flare_last_device_status(ws, stream)
+    if st != 0:
+        raise b.FlareError(st, where + " (device status)")
 
 
 def flare_attention_fwd(Q, K, V, lengths=None, q_lengths=None, q_offsets=None, documents=None, prefix=None,
@@ -96,22 +84,32 @@ def flare_attention_fwd(Q, K, V, lengths=None, q_lengths=None, q_offsets=None, d
     = lengths - 1.  ``L_out`` (float32 [B,Hq,Nq]) receives the rows'
     log-sum-exps.  With ``device_check`` the device status is read after the
     call (synchronises); its only error is an expired bounded wait."""
-    return _forward("flare_attention_fwd", Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal,
-                    scale, cap, Y, L_out, workspace, stream, check, device_check)
+    head, sizes, dev = _head(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap,
+                             check)
+    Y, y = _output("Y", Y, Q, dev, stream, check)
+    if L_out is None:
+        L = 0
+    else:
+        L = check_small("L", L_out, _f32, Q.shape[:3], dev) if check else L_out.data_ptr()
+    ws = _ws(workspace, flare_attention_workspace_bytes(*sizes), Q, stream)
+    args = _ARGS.pack(*head, *y, L, *_NO_BACKWARD)
+    call("flare_attention_fwd", "flare_attention_fwd", dev, stream, args, ws.data_ptr(), ws.numel())
+    if device_check:
+        _device_check(ws, stream, "flare_attention_fwd")
+    return Y
 
 
 def flare_attention_fwd_train(Q, K, V, lengths=None, q_lengths=None, q_offsets=None, documents=None, prefix=None,
                               slopes=None, causal: bool = False, scale: float = 0.0, cap: float = 0.0, Y=None,
                               L_out=None, workspace=None, stream=None, check: bool = True, device_check: bool = False):
     """flare_attention_fwd that returns (Y, L), what flare_attention_bwd takes."""
-    L = L_out
-    if L is None:
-        L = torch.empty(Q.shape[:3], dtype=_f32, device=Q.device)
+    if L_out is None:
+        L_out = torch.empty(Q.shape[:3], dtype=_f32, device=Q.device)
         if stream is not None:
-            L.record_stream(stream)
-    Y = _forward("flare_attention_fwd_train", Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes,
-                 causal, scale, cap, Y, L, workspace, stream, check, device_check)
-    return Y, L
+            L_out.record_stream(stream)
+    Y = flare_attention_fwd(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap, Y,
+                            L_out, workspace, stream, check, device_check)
+    return Y, L_out
 
 
 def flare_attention_bwd(Q, K, V, Y, L, dY, lengths=None, q_lengths=None, q_offsets=None, documents=None, prefix=None,
@@ -135,7 +133,8 @@ def flare_attention_bwd(Q, K, V, Y, L, dY, lengths=None, q_lengths=None, q_offse
     ws = _ws(workspace, flare_attention_workspace_bytes(*sizes, backward=True), Q, stream)
     args = _ARGS.pack(*head, *y, L.data_ptr(), *dy, *dq, *dk, *dv)
     call("flare_attention_bwd", "flare_attention_bwd", dev, stream, args, ws.data_ptr(), ws.numel())
-    _device_check(device_check, ws, stream, "flare_attention_bwd")
+    if device_check:
+        _device_check(ws, stream, "flare_attention_bwd")
     return dQ, dK, dV
 
 

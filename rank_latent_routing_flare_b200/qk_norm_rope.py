@@ -21,6 +21,7 @@ from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, entry, n
 # flare_qk_norm_rope_args
 _ARGS = struct.Struct("=9qd3q4q4q2q2q4q4q4q4q2q")
 _f32, _i32 = torch.float32, torch.int32
+_NO_BACKWARD = NO_ROWS * 2 + (0, 0)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -29,8 +30,6 @@ def flare_qk_norm_rope_workspace_bytes(B: int, N: int, Hq: int, Hk: int, D: int)
 
 
 def _check_gain(name, g, H, D, dev):
-    if g is None:
-        return 0
     if H == 0:
         raise ValueError(f"{name} is given without its tensor")
     return check_small(name, g, _f32, (D,) if g.dim() == 1 else (H, D), dev)
@@ -59,10 +58,10 @@ def _head(Q, K, q_gain, k_gain, freqs, positions, lengths, eps, interleaved, che
             raise ValueError(f"D is {D}, expected one of {ROW_WIDTHS}")
         q = NO_ROWS if Q is None else check_rows("Q", Q, (B, Hq, N, D), dev)
         k = NO_ROWS if K is None else check_rows("K", K, (B, Hk, N, D), dev)
-        gq = _check_gain("q_gain", q_gain, Hq, D, dev)
-        gk = _check_gain("k_gain", k_gain, Hk, D, dev)
-        fp = check_small("freqs", freqs, _f32, None, dev)
-        n = check_small("lengths", lengths, _i32, (B,), dev)
+        gq = 0 if q_gain is None else _check_gain("q_gain", q_gain, Hq, D, dev)
+        gk = 0 if k_gain is None else _check_gain("k_gain", k_gain, Hk, D, dev)
+        fp = 0 if freqs is None else check_small("freqs", freqs, _f32, None, dev)
+        n = 0 if lengths is None else check_small("lengths", lengths, _i32, (B,), dev)
         pp = 0
         if freqs is None:
             if positions is not None:
@@ -110,7 +109,7 @@ def flare_qk_norm_rope_fwd(Q=None, K=None, q_gain=None, k_gain=None, freqs=None,
     head, (*_, dev) = _head(Q, K, q_gain, k_gain, freqs, positions, lengths, eps, interleaved, check)
     Qr, q = _side("Qr", Qr, Q, dev, stream, check)
     Kr, k = _side("Kr", Kr, K, dev, stream, check)
-    args = _ARGS.pack(*head, *q, *k, *NO_ROWS, *NO_ROWS, 0, 0)
+    args = _ARGS.pack(*head, *q, *k, *_NO_BACKWARD)
     call("flare_qk_norm_rope_fwd", "flare_qk_norm_rope_fwd", dev, stream, args)
     return Qr, Kr
 
