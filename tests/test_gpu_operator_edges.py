@@ -1,7 +1,9 @@
 """Calls at the edges of what the attention and the preparation of queries and
 keys allow: caps so large that they hardly bend a score, long packed
 sequences, other streams, captured autograd, two calls at once."""
-import math
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -204,3 +206,31 @@ def test_offsets_beyond_32_bits():
     back = fl.flare_qk_norm_rope_bwd(Q, K, Qr, Kr, freqs=freqs)
     got = fl.flare_qk_norm_rope_bwd(rows(0), rows(1), rows(2), rows(3), freqs=freqs)
     assert torch.equal(got["dQ"], back["dQ"]) and torch.equal(got["dK"], back["dK"])
+
+
+FIRST = """
+import torch, rank_latent_routing_flare_b200 as fl
+Q, K, V = (torch.randn(1, 4, 300, 64, device='cuda').bfloat16() for _ in range(3))
+gain, freqs = torch.ones(64, device='cuda'), torch.rand(32, device='cuda')
+ids = torch.zeros(1, 300, dtype=torch.int32, device='cuda')
+def step():
+    leaves = [t.detach().requires_grad_() for t in (Q, K, V)]
+    Qr, Kr = fl.flare_qk_norm_rope(leaves[0], leaves[1], gain, gain, freqs)
+    Y = fl.flare_attention(Qr, Kr, leaves[2], documents=ids, causal=True)
+    return (Y, fl.flare_attention_fwd(Q[:, :, -1:], K, V), *torch.autograd.grad(Y, leaves, V))
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = step()
+graph.replay()
+want = step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, want))
+print('same')
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing has been loaded, and the backward's thread has no context yet, when the capture begins."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
