@@ -186,18 +186,24 @@ __device__ __forceinline__ float biased_weights(const uint32_t (&s)[N], float c2
   return x + y;
 }
 // As weights<N, true>, for capped scores of raw products: tanh and the shift
-// by the base in one polynomial.  Needs small.
-template <int N>
-__device__ __forceinline__ float capped_weights(const uint32_t (&s)[N], const ScoreOps& ops, float base, uint32_t col) {
+// by the base in one polynomial.  Needs small.  MASKED: 0 outside columns [first, last).
+template <int N, bool MASKED>
+__device__ __forceinline__ float capped_weights(const uint32_t (&s)[N], const ScoreOps& ops, float base, int first, int last,
+                                                uint32_t col) {
   const uint64_t nb = f2_dup(-base);
   uint64_t sum0 = f2_dup(0.f), sum1 = sum0;
 #pragma unroll
   for (int k = 0; k < N; k += 32) {
     uint32_t pk[16];
+    const uint32_t bits = MASKED ? column_bits(first, last, k) : ~0u;
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
       float p0, p1;
       ex2_pair(ops.poly(f2(s[k + 2 * q], s[k + 2 * q + 1]), nb), p0, p1);
+      if (MASKED) {
+        p0 = bits & (1u << (2 * q)) ? p0 : 0.f;
+        p1 = bits & (2u << (2 * q)) ? p1 : 0.f;
+      }
       if (q & 1) sum1 = f2_add(sum1, f2_pack(p0, p1));
       else sum0 = f2_add(sum0, f2_pack(p0, p1));
       pk[q] = pack_bf16x2(p0, p1);
@@ -421,11 +427,18 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
         if (masked) hide<KT>(s, first, last);
         mx = max_of(s) * ops.c2;
       } else if (MOD == 1) {
-        // tanh grows with its argument: the maximum takes it once
+        // tanh grows with its argument: the maximum takes it once.  D <= 64:
+        // hidden columns count too (under a cap of up to 55 they lie at most
+        // 2^80 above the others, which no fp32 or bf16 weight minds) and get
+        // their zeros behind the exponential: 12 documents in 8192 keys 177 -> 162
+        // us.  A row's largest weight is then no exact 1: its rounding to bf16 adds
+        // up to as much again as the output's.  At D = 128 the second body costs
+        // more than it saves (prefixes 208 -> 215).
         mx = max_of(s);
-        small = __all_sync(~0u, ops.small(fmaxf(mx, -min_of(s))));
-        if (masked || !small) {
-          cap_scores<KT>(s, ops, small, 0.f);
+        const bool poly = __all_sync(~0u, ops.small(fmaxf(mx, -min_of(s))));
+        small = poly && (!masked || (D < 128 && ops.out <= 80.f));
+        if (!small) {
+          cap_scores<KT>(s, ops, poly, 0.f);
           if (masked) hide<KT>(s, first, last);
           mx = max_of(s);
         } else {
@@ -481,8 +494,9 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
         for (int k = 0; k < KT; k += 32) tmem_st16(col_s + k / 2, none);
       } else if (MOD == 2 && how == kLinear) {
         sum = biased_weights<KT>(s, capped ? 1.f : ops.c2, base, static_cast<float>(pos - k0), slope2, linear_side, col_s);
-      } else if (MOD == 1 && small && !masked) {
-        sum = capped_weights<KT>(s, ops, base, col_s);
+      } else if (MOD == 1 && small) {
+        if (D < 128 && masked) sum = capped_weights<KT, true>(s, ops, base, first, last, col_s);
+        else sum = capped_weights<KT, false>(s, ops, base, first, last, col_s);
       } else {
         sum = weights<KT, MOD == 0>(s, ops.c2, base, col_s);
       }

@@ -41,6 +41,26 @@ def test_a_tiny_cap(cap):
         check(*make(2, 2, 1, Nq, 200, 64, seed=21, cap=cap, causal=True, lengths=i32(200, 77)), backward=Nq > 2)
 
 
+@pytest.mark.parametrize("cap", [30.0, 55.0, 56.0, 90.0])
+def test_hidden_scores_far_above_the_visible(cap):
+    """The keys behind a row score near half the cap, the ones it sees near minus half of it; some hidden keys are
+    NaN or infinite.  On either side of the cap up to which hidden columns count for a tile's reference."""
+    g = torch.Generator(device=DEV).manual_seed(31)
+    for D in (16, 64, 128):
+        N, edge = 500, 250
+        Q = torch.full((1, 2, N, D), 1.0, device=DEV).bfloat16()
+        K = torch.randn(1, 2, N, D, generator=g, device=DEV) * 0.1
+        K[:, :, :edge] -= 0.45 * cap / D ** 0.5
+        K[:, :, edge:] += 0.45 * cap / D ** 0.5
+        V = torch.randn(1, 2, N, D, generator=g, device=DEV).bfloat16()
+        o = {"cap": cap, "prefix": i32(edge), "causal": True, "q_offsets": i32(-1000)}
+        check(Q, K.bfloat16(), V, torch.randn(1, 2, N, D, generator=g, device=DEV).bfloat16(), o)
+        ids = torch.zeros(1, N, dtype=torch.int32, device=DEV)
+        ids[:, edge:] = -1                                       # check puts NaN and infinities there
+        o = {"cap": cap, "documents": ids}
+        check(Q, K.bfloat16(), V, torch.randn(1, 2, N, D, generator=g, device=DEV).bfloat16(), o)
+
+
 @pytest.mark.parametrize("slope", [-0.05, 0.0, 3.0])
 def test_slopes_of_any_sign(slope):
     """A negative slope prefers distant keys; a zero one is no bias."""
