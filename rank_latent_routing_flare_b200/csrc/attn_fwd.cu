@@ -372,6 +372,9 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
             }
             if (ok && n + 1 >= a[w] && n + 1 < e[w]) ok = issue_s(w, n + 1);
           }
+          // a tile between the two ranges (documents can leave it out): its
+          // copy lands before its stage is given back
+          if (ok && (n < a[0] || n >= e[0]) && (n < a[1] || n >= e[1])) ok = mbar_wait_warp(kv_full + st, (n / NST) & 1, wc);
           if (elect_one()) umma_commit(kv_empty + st);
           __syncwarp();
         }

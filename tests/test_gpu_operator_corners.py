@@ -1,0 +1,50 @@
+"""Operators around the mixer where masks, epsilons, scales and memory are
+unusual, against their definition in 64 bits."""
+import math
+
+import pytest
+import torch
+
+import rank_latent_routing_flare_b200 as fl
+
+from . import attention_ref as ref
+from .test_gpu_attention import DEV, documents, i32, make
+
+pytestmark = pytest.mark.gpu
+
+
+def hide_unseen(Q, K, V, dY, opts):
+    """NaN and infinities in every key that no row sees and every row that sees no key."""
+    B, _, Nq, _ = Q.shape
+    masks = {n: opts[n] for n in ("lengths", "q_lengths", "q_offsets", "documents", "prefix", "causal") if n in opts}
+    ok, _ = ref.visible(B, Nq, K.shape[2], DEV, **masks)
+    no_key, no_row = ~ok.any(1).view(B, 1, -1, 1), ~ok.any(2).view(B, 1, -1, 1)
+    for x, m, bad in ((K, no_key, math.nan), (V, no_key, math.inf), (Q, no_row, math.nan), (dY, no_row, -math.inf)):
+        x.masked_fill_(m, bad)
+    return Q, K, V, dY, opts
+
+
+def check(Q, K, V, dY, opts, backward=True):
+    want = ref.attention(Q, K, V, dY=dY if backward else None, **opts)
+    Y, L = fl.flare_attention_fwd_train(Q, K, V, device_check=True, **opts)
+    ref.close(Y, want["Y"], "Y")
+    ref.close(L, want["L"], "L")
+    if backward:
+        for name, got in zip(("dQ", "dK", "dV"), fl.flare_attention_bwd(Q, K, V, Y, L, dY, device_check=True, **opts)):
+            ref.close(got, want[name], name)
+
+
+@pytest.mark.parametrize("D", [16, 32, 64, 128])
+@pytest.mark.parametrize("N,cuts,dead,lengths", [
+    (256, (60, 128), (1,), None),               # rows 60 .. 127 in no document: keys 64 .. 127 between two tiles' ranges
+    (700, (60, 128, 316, 384), (1, 3), None),
+    (2048, (1664, 1728), (), 100),              # documents beyond the length
+    (2048, (40, 192, 1664, 1728), (1,), 1700),
+])
+def test_query_tiles_whose_keys_lie_apart(N, cuts, dead, lengths, D):
+    """Keys between the ranges of a CTA's two query tiles, which neither of them takes part in."""
+    o = {"documents": documents(2, N, cuts, dead)}
+    if lengths:
+        o["lengths"] = i32(lengths, N)
+    for more in ({}, {"cap": 9.0}, {"bias": True}):
+        check(*hide_unseen(*make(2, 2, 1, N, N, D, seed=N + D, **o, **more)), backward=not more)
