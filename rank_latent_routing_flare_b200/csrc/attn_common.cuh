@@ -43,7 +43,9 @@ __device__ __forceinline__ BatchMask batch_mask(const AttnMask& m, int b) {
   r.doc = m.doc ? m.doc + static_cast<long>(b) * m.Nk : nullptr;
   return r;
 }
-// Keys [x, y) that row i sees (x = y: none).
+// Keys [x, y) that row i sees (x = y: none).  Neither end lies behind the
+// length, not for a row that sees nothing either: kernels visit what lies
+// between the first row's and the last row's ends, and that is no padding.
 __device__ __forceinline__ int2 row_interval(const BatchMask& m, int i) {
   const long p = m.off + i;
   long lo = 0, hi = m.len;
@@ -52,10 +54,10 @@ __device__ __forceinline__ int2 row_interval(const BatchMask& m, int i) {
     if (p < 0) {
       hi = 0;
     } else if (p >= m.nk) {
-      lo = hi = m.nk;
+      lo = hi = m.len;
     } else {
       const int2 d = m.doc[p];
-      lo = d.x;
+      lo = min(d.x, m.len);
       hi = min(hi, static_cast<long>(d.y));
     }
   }

@@ -8,7 +8,7 @@ import torch
 import rank_latent_routing_flare_b200 as fl
 
 from . import attention_ref as ref
-from .test_gpu_attention import DEV, documents, i32, make
+from .test_gpu_attention import DEV, check as check_poisoned, documents, i32, make
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,14 @@ def test_query_tiles_whose_keys_lie_apart(N, cuts, dead, lengths, D):
         o["lengths"] = i32(lengths, N)
     for more in ({}, {"cap": 9.0}, {"bias": True}):
         check(*hide_unseen(*make(2, 2, 1, N, N, D, seed=N + D, **o, **more)), backward=not more)
+
+
+@pytest.mark.parametrize("D", [16, 32, 64, 128])
+def test_few_rows_whose_document_lies_behind_the_length(D):
+    """The last rows see nothing, their documents beginning behind lengths: what lies in between is padding."""
+    ids = documents(2, 8, (5,))
+    check_poisoned(*make(2, 1, 1, 8, 8, D, seed=41, documents=ids, lengths=i32(4, 2)), backward=False)
+    ids = documents(2, 900, (300, 450, 700))
+    for off in (i32(446, 296), i32(898, 697)):
+        o = dict(documents=ids, lengths=i32(430, 777), q_offsets=off)
+        check_poisoned(*make(2, 4, 2, 8, 900, D, seed=42, **o), backward=False)
