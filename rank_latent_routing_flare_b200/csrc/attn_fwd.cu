@@ -453,14 +453,16 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
         const float c = capped ? 1.f : ops.c2;
         // A tile that every row sees, all on one side: no score is above the
         // largest product with the smallest distance's bias (a negative
-        // slope's largest).  Weights below 2^-64 of the reference change no
-        // fp32 sum: such a tile's are 0 (but a NaN is kept).  Otherwise the bound serves as the
-        // maximum where it is not far above it.
+        // slope's largest).  The bound serves as the maximum where it is at
+        // most 2^64 above it (`slack`); the row's sum is then at least
+        // 2^-slack of the reference, and weights below 2^-64 of that change
+        // no fp32 sum: a tile of such weights gets zeros (but a NaN is kept).
         if (side != 0 && !masked) {
           const int near = side > 0 ? pos - (k0 + KT - 1) : k0 - pos;
           mx = fmaf(max_of<KT, true>(s), c, -slope2 * static_cast<float>(slope2 >= 0.f ? near : near + KT - 1));
-          const bool steep = fabsf(slope2) * (KT - 1) > 64.f;
-          how = it > 0 && __all_sync(~0u, mx < m - 64.f) ? kNone : steep ? kExact : kLinear;
+          const float slack = fabsf(slope2) * (KT - 1);
+          const bool steep = slack > 64.f;                    // references of this row are maxima
+          how = it > 0 && __all_sync(~0u, mx < m - (steep ? 64.f : 64.f + slack)) ? kNone : steep ? kExact : kLinear;
         }
         if (how == kExact) {
           bias_scores<KT>(s, c, static_cast<float>(pos - k0), slope2, side);

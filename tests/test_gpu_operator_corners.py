@@ -59,3 +59,28 @@ def test_few_rows_whose_document_lies_behind_the_length(D):
     for off in (i32(446, 296), i32(898, 697)):
         o = dict(documents=ids, lengths=i32(430, 777), q_offsets=off)
         check_poisoned(*make(2, 4, 2, 8, 900, D, seed=42, **o), backward=False)
+
+
+@pytest.mark.parametrize("D", [16, 64, 128])
+@pytest.mark.parametrize("slope", [0.3, 0.34, 0.35, 0.36])
+@pytest.mark.parametrize("cap", [0.0, 120.0])
+def test_a_large_score_at_the_far_end_of_a_tile(slope, cap, D):
+    """Keys on either side of a tile's border outweigh all others, though the nearer of them is the farthest of its
+    tile: the tile's largest product and its smallest distance belong to different keys."""
+    N = 512
+    Q, K, V, dY, _ = make(1, 2, 1, N, N, D, seed=D)
+    Q.zero_()
+    Q[..., 0] = 1
+    o = {"slopes": torch.full((2,), slope, device=DEV), "causal": True, "scale": 1.0, "cap": cap}
+    for border in (128, 256):
+        for rivals, score in ((1, 48.5), (10, 49.0), (100, 49.0)):
+            K.zero_()
+            K[:, :, border, 0], K[:, :, border - rivals:border, 0] = 50.0, score
+            check(Q, K, V, dY, o)
+
+
+@pytest.mark.parametrize("slope", [0.02, 0.1, 0.3, 0.5])
+def test_moderate_slopes_and_large_scores(slope):
+    for D in (32, 128):
+        Q, K, V, dY, _ = make(1, 4, 2, 700, 700, D, seed=40, qscale=12.0)
+        check(Q, K, V, dY, {"slopes": slope * torch.tensor([1.0, 0.9, 1.1, -0.5], device=DEV), "causal": True})
