@@ -396,7 +396,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kWarpsPerSM / kMaxWarps) norm_
         const int t = t0 + i * step;
         if (t - at.t_in >= w.ntok) break;   // uniform over the warp
         Vec16& x16 = v[i];
-        const float r = rsqrtf(fmaf(row_sum<D>(dot16(x16, x16)), 1.0f / D, p.eps));
+        // 0 for a lane without a row: it adds nothing to the gains' gradients, whatever eps is
+        const float mean = fmaf(row_sum<D>(dot16(x16, x16)), 1.0f / D, p.eps), r = t < w.nvalid ? rsqrtf(mean) : 0.f;
         const uint64_t r2 = f2_dup(r);
         if constexpr (!BWD) {
 #pragma unroll

@@ -9,6 +9,7 @@ import rank_latent_routing_flare_b200 as fl
 
 from . import attention_ref as ref
 from .test_gpu_attention import DEV, check as check_poisoned, documents, i32, make
+from .test_gpu_qk_norm_rope import STEP, angles, close, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +85,25 @@ def test_moderate_slopes_and_large_scores(slope):
     for D in (32, 128):
         Q, K, V, dY, _ = make(1, 4, 2, 700, 700, D, seed=40, qscale=12.0)
         check(Q, K, V, dY, {"slopes": slope * torch.tensor([1.0, 0.9, 1.1, -0.5], device=DEV), "causal": True})
+
+
+@pytest.mark.parametrize("D", [16, 32, 64, 128])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_gain_gradients_without_an_epsilon(interleaved, D):
+    """eps = 0: padding, and lanes without a row, add nothing to the gains' gradients."""
+    g = torch.Generator(device=DEV).manual_seed(44)
+    for B, N, H, lengths, shape in ((1, 1, 1, None, (D,)), (3, 37, 3, (37, 0, 5), (3, D)), (2, 700, 4, (699, 130), (D,))):
+        x, dy = (torch.randn(B, H, N, D, generator=g, device=DEV).bfloat16() for _ in range(2))
+        gain, freqs = 1 + 0.2 * torch.randn(shape, generator=g, device=DEV), torch.rand(D // 2, generator=g, device=DEV)
+        n = None if lengths is None else i32(*lengths)
+        got = fl.flare_qk_norm_rope_bwd(x, None, dy, None, gain, freqs=freqs, lengths=n, eps=0.0, interleaved=interleaved)
+        want, tol = 0, 0
+        for b in range(B):     # each entry's live rows on their own: the definition has no padding there
+            m = N if lengths is None else lengths[b]
+            if m:
+                a = angles(m, freqs, None, 1)
+                dx, dtol, dg, gt = reference(x[b:b + 1, :, :m], gain, a, None, 0.0, interleaved, dy=dy[b:b + 1, :, :m])
+                close(got["dQ"][b:b + 1, :, :m], dx, dtol, "dQ")
+                want, tol = want + dg, tol + gt
+            assert (got["dQ"][b, :, m:] == 0).all()
+        close(got["dq_gain"], want, tol * (1 + B * H * N * STEP) + B * H * N * STEP * want.abs(), "dq_gain")
