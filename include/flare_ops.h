@@ -104,10 +104,11 @@ FLARE_API flare_status flare_qk_norm_rope_bwd(const flare_qk_norm_rope_args* arg
  * Y_i = softmax_j(s) V, L_i = log sum_j exp(s).  A row that sees no key has
  * Y_i = 0, L_i = -inf and zero gradients, and contributes none.
  *
- * Keys that no row may see (j >= lengths[b], ids below zero) and rows i >=
- * q_lengths[b] may hold anything, infinities and NaN included.  A NaN or an
- * infinity in a V row that some row of the head sees may also reach rows that
- * mask it (0 times it is NaN, as in softmax(s) V).
+ * Keys that no row sees (j >= lengths[b], ids below zero, other documents than
+ * the rows', slots of a cache behind the newest token of a causal call) and
+ * rows i >= q_lengths[b] may hold anything, infinities and NaN included.  A NaN
+ * or an infinity in a row that takes part may also reach rows and keys that the
+ * masks keep from it (0 times it is NaN, as in softmax(s) V).
  *
  * The cap is 0 or lies in [1e-6, 1e9]; Nq and Nk are at most 2^27.  Products
  * of bf16 rows, exponentials, sums and statistics are fp32; weights and dS

@@ -78,7 +78,7 @@ def flare_attention_fwd(Q, K, V, lengths=None, q_lengths=None, q_offsets=None, d
     lengths[b], i < q_lengths[b] (int32 [B]), with ``causal`` j <= p or j <
     prefix[b] (int32 [B]), and with ``documents`` (int32 [B,Nk]) j and p lie in
     the same run of equal ids >= 0.  A row that sees nothing comes out as zeros;
-    keys that no row may see and rows behind q_lengths may hold anything.
+    keys that no row sees and rows behind q_lengths may hold anything.
 
     One new token over a cache: Nq = 1, lengths = tokens in the cache, q_offsets
     = lengths - 1.  ``L_out`` (float32 [B,Hq,Nq]) receives the rows'

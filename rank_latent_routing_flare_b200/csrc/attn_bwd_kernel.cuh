@@ -38,8 +38,9 @@
 // pass: there up to eight CTAs, a cluster, share a tile's stream and add their
 // partial sums in a fixed order over each other's shared memory.
 //
-// Streamed rows that take no part (padding) are zeroed in shared memory
-// before the products read them: a weight of 0 does not erase a NaN.
+// Streamed rows that take no part (padding; in the dQ pass every key that no
+// row of the tile sees) are zeroed in shared memory before the products read
+// them: a weight of 0 does not erase a NaN.
 //
 // D >= 64: T = 64, up to 512 TMEM columns, one CTA per SM.  D <= 32: T = 48, 256
 // columns, two CTAs per SM; the exponentials bound those.  Measured, dQ and
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
   uint64_t* all_done = p_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Cfg::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(sm + Cfg::OFF_MISC + 4);
-  volatile int* range = reinterpret_cast<volatile int*>(sm + Cfg::OFF_MISC + 8);       // [4]
+  volatile int* range = reinterpret_cast<volatile int*>(sm + Cfg::OFF_MISC + 8);       // [6]
   volatile int* last_load = reinterpret_cast<volatile int*>(sm + Cfg::OFF_MISC + 32);  // [NST]
 
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -142,8 +143,9 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
 
   // Stream tiles [range0, range1) that take part, and of the stream's rows those
   // [range2, range3) that every row of this tile that takes part sees (dQ
-  // pass), or that see all of its keys.
-  if (threadIdx.x < 4) {
+  // pass), or that see all of its keys.  dQ pass: the first and the last key
+  // that one of them sees, [range4, range5).
+  if (threadIdx.x < (KV ? 4 : 6)) {
     const int what = threadIdx.x;
     int v = 0;
     if (KV) {   // hi > x0 from the first row on, lo < x0 + 128 up to the last; hi >= x0 + 128, lo <= x0
@@ -159,7 +161,8 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
       const int r1 = min(x0 + 128, mask.qlen);
       if (x0 < r1) {
         const int2 a = row_interval(mask, x0), z = row_interval(mask, r1 - 1);
-        if (a.x < z.y) v = what == 0 ? a.x / T : what == 1 ? (z.y + T - 1) / T : what == 2 ? z.x : a.y;
+        if (a.x < z.y)
+          v = what == 0 ? a.x / T : what == 1 ? (z.y + T - 1) / T : what == 2 ? z.x : what == 3 ? a.y : what == 4 ? a.x : z.y;
       }
     }
     range[what] = v;
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
         if (KV) {
           dead = rs[tid] == -INFINITY;
         } else if (y0 + tid < mask.nk) {
-          dead = y0 + tid >= mask.len;
+          dead = y0 + tid < range[4] || y0 + tid >= range[5];
           if (mask.doc) {
             const int2 d = mask.doc[y0 + tid];
             dead |= d.x == d.y;

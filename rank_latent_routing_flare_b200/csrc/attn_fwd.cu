@@ -24,8 +24,9 @@
 // Tiles outside [lo of the first row, hi of the last) are not visited; the
 // interval is tested per element only in tiles that some row of the warp does
 // not see whole.  A weight of 0 does not erase a NaN in V, so rows of V that
-// no query may see (padding) are zeroed in shared memory by the softmax
-// threads before the product.
+// no row of the CTA sees (padding, other documents, slots of a cache behind
+// the newest token) are zeroed in shared memory by the softmax threads before
+// the product.
 //
 // D = 128, and capped or biased scores: KT = 128, 512 TMEM columns, one CTA per
 // SM whose softmax threads take over most of its registers.  Plain scores of D
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
   uint64_t* all_done = o_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Cfg::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(sm + Cfg::OFF_MISC + 4);
-  volatile int* range = reinterpret_cast<volatile int*>(sm + Cfg::OFF_MISC + 8);       // [4]
+  volatile int* range = reinterpret_cast<volatile int*>(sm + Cfg::OFF_MISC + 8);       // [6]
   volatile int* last_load = reinterpret_cast<volatile int*>(sm + Cfg::OFF_MISC + 32);  // [NST]
 
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -253,6 +254,11 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
     const int2 r = tile_range(mask, q0 + threadIdx.x * QT, KT);
     range[2 * threadIdx.x] = r.x;
     range[2 * threadIdx.x + 1] = r.y;
+  }
+  if (threadIdx.x == 32) {   // the keys from the first to the last that a row of the CTA sees
+    const int r1 = min(q0 + NQ * QT, mask.qlen);
+    range[4] = q0 < r1 ? row_interval(mask, q0).x : 0;
+    range[5] = q0 < r1 ? row_interval(mask, r1 - 1).y : 0;
   }
   if (threadIdx.x == 64) {
     for (int i = 0; i < 2; ++i) {
@@ -400,13 +406,14 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     const int a_w = w ? a[1] : a[0], n_w = (w ? e[1] : e[0]) - a_w;
+    const int seen0 = range[4], seen1 = range[5];
     for (int it = 0; it < n_w; ++it) {
       const int n = a_w + it, k0 = key0(n), st = n % NST;
-      // the V row this thread answers for: a key that no query may see
+      // the V row this thread answers for: a key that no row of the CTA sees
       bool dead = false;
       if (KT == 128 || tid < KT) {
         const int key = k0 + tid;
-        dead = key >= mask.len && key < mask.nk;
+        dead = (key < seen0 || key >= seen1) && key < mask.nk;
         if (mask.doc && key < mask.nk) {
           const int2 d = mask.doc[key];
           dead |= d.x == d.y;

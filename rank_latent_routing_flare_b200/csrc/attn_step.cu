@@ -77,17 +77,17 @@ __device__ __forceinline__ uint32_t transposed(uint32_t a) {
   return r;
 }
 
-// Copies of a chunk's rows of K and V, zeros from key `end` on.
+// Copies of a chunk's rows of K and V, zeros from key `end` on and for V's before `beg`.
 template <int D>
 __device__ __forceinline__ void load_chunk(uint32_t dst, const StepParams& p, const BatchMask& m, const uint16_t* kb,
-                                           const uint16_t* vb, int key0, int end) {
+                                           const uint16_t* vb, int key0, int beg, int end) {
   using C = StepCfg<D>;
   constexpr int ROWS = 32 / C::U, N = kChunk / ROWS;   // rows a warp copies at once
   const int lane = threadIdx.x & 31, r0 = lane / C::U, u = lane % C::U;
   const uint32_t at0 = 2 * D * r0 + 16 * (u ^ C::swizzle(r0));
   auto at = [&](int i) { return dst + (at0 ^ 16 * C::swizzle(i * ROWS)) + 2 * D * ROWS * i; };
   const uint16_t *k = kb + static_cast<long>(key0 + r0) * p.k.sn + 8 * u, *v = vb + static_cast<long>(key0 + r0) * p.v.sn + 8 * u;
-  if (key0 + kChunk <= end && !m.doc) {
+  if (key0 >= beg && key0 + kChunk <= end && !m.doc) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       copy16(at(i), k);
@@ -102,7 +102,8 @@ __device__ __forceinline__ void load_chunk(uint32_t dst, const StepParams& p, co
     const int key = key0 + r0 + i * ROWS;
     bool ok = key < end;
     copy16(at(i), ok ? k + i * ROWS * p.k.sn : kb, ok);
-    if (m.doc && ok) {   // a weight of 0 does not erase a NaN: padding inside the range is not read
+    ok = ok && key >= beg;   // a weight of 0 does not erase a NaN: what no row sees is not read
+    if (m.doc && ok) {
       const int2 d = m.doc[key];
       ok = d.x != d.y;
     }
@@ -123,11 +124,12 @@ __global__ void __launch_bounds__(kStepWarps * 32, StepCfg<D>::CTAS) attn_step_k
   const BatchMask mask = batch_mask(a.mask, b);
 
   // the keys that any row sees, rounded to chunks and dealt to the splits
-  int lo = 0, hi = 0;
+  int seen = 0, lo = 0, hi = 0;
   const int last_row = min(a.mask.Nq, mask.qlen) - 1;
   if (blockIdx.x == 0 && threadIdx.x < 4) a.err[threadIdx.x] = 0u;   // nothing here can wait in vain
   if (last_row >= 0) {
-    lo = row_interval(mask, 0).x / kChunk * kChunk;
+    seen = row_interval(mask, 0).x;
+    lo = seen / kChunk * kChunk;
     hi = row_interval(mask, last_row).y;
   }
   const int chunks = hi > lo ? (hi - lo + kChunk - 1) / kChunk : 0;
@@ -140,7 +142,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, StepCfg<D>::CTAS) attn_step_k
   const int c_beg = split * per + warp;
   auto load = [&](int n) {   // the warp's chunk n
     const int c = c_beg + n * kStepWarps;
-    if (c < c_end) load_chunk<D>(ring + n % C::STAGES * 2 * C::CHUNK_B, p, mask, kb, vb, lo + c * kChunk, hi);
+    if (c < c_end) load_chunk<D>(ring + n % C::STAGES * 2 * C::CHUNK_B, p, mask, kb, vb, lo + c * kChunk, seen, hi);
     copies_end();
   };
 #pragma unroll

@@ -8,7 +8,7 @@ import torch
 import rank_latent_routing_flare_b200 as fl
 
 from . import attention_ref as ref
-from .test_gpu_attention import DEV, check as check_poisoned, documents, i32, make
+from .test_gpu_attention import DEV, check as check_poisoned, documents, i32, make, options
 from .test_gpu_qk_norm_rope import STEP, angles, close, reference
 
 pytestmark = pytest.mark.gpu
@@ -107,3 +107,28 @@ def test_gain_gradients_without_an_epsilon(interleaved, D):
                 want, tol = want + dg, tol + gt
             assert (got["dQ"][b, :, m:] == 0).all()
         close(got["dq_gain"], want, tol * (1 + B * H * N * STEP) + B * H * N * STEP * want.abs(), "dq_gain")
+
+
+UNSEEN = {
+    # B, Hq, Hk, Nq, Nk, options
+    "cache": (2, 4, 2, 1, 700, {"causal": True, "q_offsets": (300, 17)}),
+    "cache_rows": (3, 4, 2, 4, 700, {"causal": True, "q_offsets": (300, 14, -2)}),
+    "cache_documents": (2, 4, 2, 3, 700, {"documents": ((101, 333, 500), ()), "q_offsets": (120, 400)}),
+    "cache_prefix": (2, 2, 2, 2, 700, {"causal": True, "prefix": (45, 333), "q_offsets": (20, 20)}),
+    "chunk": (2, 4, 2, 200, 1500, {"causal": True, "q_offsets": (77, 900)}),
+    "chunk_bias": (2, 4, 2, 200, 1500, {"causal": True, "q_offsets": (77, 900), "bias": True}),
+    "chunk_cap": (2, 4, 2, 300, 700, {"causal": True, "q_offsets": (33, 100), "cap": 20.0, "prefix": (0, 450)}),
+    "chunk_documents": (2, 4, 2, 300, 1500, {"documents": ((101, 333, 701), ()), "q_offsets": (120, 650)}),
+    "chunk_padded": (2, 2, 1, 300, 600, {"causal": True, "q_offsets": (10, 200), "q_lengths": (140, 0),
+                                         "lengths": (600, 300)}),
+    "split": (1, 1, 1, 40, 5000, {"causal": True, "q_offsets": (3003,)}),
+}
+
+
+@pytest.mark.parametrize("D", [16, 32, 64, 128])
+@pytest.mark.parametrize("name", UNSEEN)
+def test_keys_that_no_row_sees_may_hold_anything(name, D):
+    """A cache's slots behind the newest token, other documents than the rows': as padding, they are not read into any
+    result."""
+    B, Hq, Hk, Nq, Nk, o = UNSEEN[name]
+    check(*hide_unseen(*make(B, Hq, Hk, Nq, Nk, D, seed=Nk + D, **options(o, B, Nk))))
