@@ -5,6 +5,35 @@
 namespace flare {
 namespace {
 
+// A row's largest score, in log2 units over biased positions, by the row's
+// lanes, a key each.  It stands in for the log-sum-exp of a row so far from
+// its keys that L, about -slope times that distance, has no bits left for the
+// scores (the dQ pass divides by the sum of the weights in any case).  Slow,
+// and rare: a row 2^24 / slope tokens or more from the nearest key it sees.
+constexpr float kFarBias = 0x1p24f;   // up to here L is off by one at most
+template <int D>
+__device__ __noinline__ float largest_score(const AttnBwdParams& bp, int b, int h, int i, int2 iv, int pos, int l) {
+  const AttnParams& p = bp.a;
+  const ScoreOps ops(p.scale, p.cap, true);
+  const uint4* q = reinterpret_cast<const uint4*>(bp.q.p + b * bp.q.sb + h * bp.q.sh + i * bp.q.sn);
+  const uint16_t* k = bp.k.p + b * bp.k.sb + h / p.G * bp.k.sh;
+  float top = -INFINITY;
+  for (int j = iv.x + l; j < iv.y; j += D / 8) {
+    const uint4* kj = reinterpret_cast<const uint4*>(k + j * bp.k.sn);
+    float s = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 x = q[c], y = kj[c];
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s = fmaf(bf16_lo(u[e]), bf16_lo(v[e]), fmaf(bf16_hi(u[e]), bf16_hi(v[e]), s));
+    }
+    s = p.cap > 0.f ? ops.capped(s) : s * ops.c2;
+    top = fmaxf(top, fmaf(-p.slopes[h] * kLog2e, fabsf(static_cast<float>(pos - j)), s));
+  }
+  return top;
+}
+
 // One row's statistics: l2 = L log2(e), moved by the distance that the bias
 // positions leave out, and delta = <dY, Y> in fp32.  D / 8 lanes a row, 16-byte
 // loads.
@@ -28,6 +57,13 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const AttnBwdParams bp) 
 #pragma unroll
     for (int k = 0; k < 4; ++k) delta = fmaf(bf16_lo(u[k]), bf16_lo(v[k]), fmaf(bf16_hi(u[k]), bf16_hi(v[k]), delta));
   }
+  const int pos = bias_position(m, i, iv);
+  const bool far = sees && p.slopes && fabsf(p.slopes[h] * bias_shift(m, i, iv)) > kFarBias;
+  float top = far ? largest_score<D>(bp, b, h, i, iv, pos, l) : 0.f;
+  if (__any_sync(~0u, far)) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  }
 #pragma unroll
   for (int o = L / 2; o > 0; o >>= 1) delta += __shfl_xor_sync(~0u, delta, o);
   if (l == 0 && i < rows) {
@@ -35,14 +71,15 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const AttnBwdParams bp) 
     if (sees) {
       float L2 = p.L[bh * p.mask.Nq + i];
       if (p.slopes) L2 += p.slopes[h] * bias_shift(m, i, iv);
-      if (L2 != -INFINITY) l2 = L2 * kLog2e;
+      if (far) l2 = top;
+      else if (L2 != -INFINITY) l2 = L2 * kLog2e;
     }
     float* r = bp.rows + (bh * bp.row_blocks + i / T) * (kAttnRowFields * T) + i % T;
     r[0] = -l2;
     r[T] = l2 == INFINITY ? 0.f : -delta;
     r[2 * T] = __int_as_float(iv.x);
     r[3 * T] = __int_as_float(iv.y);
-    r[4 * T] = __int_as_float(bias_position(m, i, iv));
+    r[4 * T] = __int_as_float(pos);
   }
 }
 

@@ -132,3 +132,25 @@ def test_keys_that_no_row_sees_may_hold_anything(name, D):
     result."""
     B, Hq, Hk, Nq, Nk, o = UNSEEN[name]
     check(*hide_unseen(*make(B, Hq, Hk, Nq, Nk, D, seed=Nk + D, **options(o, B, Nk))))
+
+
+@pytest.mark.parametrize("D", [16, 128])
+@pytest.mark.parametrize("Nk", [200, 1300])
+@pytest.mark.parametrize("slope,off", [(4.0, 1 << 30), (-4.0, 1 << 30), (0.5, -(1 << 30)), (1e4, (1 << 31) - 200)])
+def test_gradients_of_rows_far_from_their_keys(slope, off, Nk, D):
+    """The distance that all keys of a row share is no part of its weights, however little of them it leaves in an
+    fp32 log-sum-exp: every row's gradients are those of one that stands at its nearest key, as one more head does."""
+    Nq = 40
+    Q, K, V, dY, _ = make(2, 1, 1, Nq, Nk, D, seed=43, layout="head")
+    if abs(slope) > 100:
+        K.mul_(0.0)     # weights that the slope alone does not decide would need scores of its size
+    o = {"slopes": torch.full((1,), slope, device=DEV), "q_offsets": i32(off, off), "lengths": i32(Nk, Nk // 3)}
+    Y, L = fl.flare_attention_fwd_train(Q, K, V, **o)
+    got = fl.flare_attention_bwd(Q, K, V, Y, L, dY, **o)
+    near = i32(Nk - 1, Nk // 3 - 1) if off > 0 else i32(0, 0)
+    folded = dict(slopes=torch.full((Nq,), slope, device=DEV), q_offsets=near, lengths=o["lengths"])
+    rows = lambda t: t.transpose(1, 2)                                  # noqa: E731  (rows of one head as heads of one row)
+    want = ref.attention(rows(Q), K, V, dY=rows(dY), **folded)
+    ref.close(rows(Y), want["Y"], "Y")
+    for name, g in zip(("dQ", "dK", "dV"), (rows(got[0]), *got[1:])):
+        ref.close(g, want[name], name)
