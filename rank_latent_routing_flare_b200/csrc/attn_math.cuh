@@ -81,18 +81,19 @@ struct ScoreOps {
   float out;          // cap log2(e)
   uint64_t k[4];      // f tanh(s u) = s (k0 + k1 w + k2 w^2 + k3 w^3), w = s^2, for |s u| <= 1/2
   __device__ __forceinline__ ScoreOps(float scale, float cap, bool times_out)
-      : c2(scale * 1.4426950408889634f), u(cap > 0.f ? scale / cap : 0.f),
-        most((u >= 1e-5f ? 0.5f : 0.0625f) / u), out(cap * 1.4426950408889634f) {
+      : c2(scale * 1.4426950408889634f), u(cap > 0.f ? scale / cap : 0.f), out(cap * 1.4426950408889634f) {
     const float f = u * (times_out ? out : 1.f), w = u * u;
     k[0] = f2_dup(0x1.ffffeep-1f * f);
     k[1] = f2_dup(-0x1.5542f2p-2f * f * w);
     k[2] = f2_dup(0x1.0e2324p-3f * f * w * w);
     k[3] = f2_dup(-0x1.6bbe38p-5f * f * w * w * w);
+    most = f * w * w * w < 1e38f ? (u >= 1e-5f ? 0.5f : 0.0625f) / u : -1.f;
   }
   // Whether products up to `top` in magnitude may take the polynomial: up to
   // half the cap.  Under a cap so large that u^7 may vanish from the
-  // coefficients, up to a sixteenth, where its term is below a rounding.  tanh_any's absolute
-  // error of 1e-7 cap is then at most 2e-6 of the largest score.
+  // coefficients, up to a sixteenth, where its term is below a rounding; under
+  // one so small that u^7 may overflow, none.  tanh_any's absolute error of 1e-7
+  // cap is then at most 2e-6 of the largest score.
   __device__ __forceinline__ bool small(float top) const { return top <= most; }
   // f tanh(s u) of two products + c
   __device__ __forceinline__ uint64_t poly(uint64_t s, uint64_t c) const {

@@ -154,3 +154,16 @@ def test_gradients_of_rows_far_from_their_keys(slope, off, Nk, D):
     ref.close(rows(Y), want["Y"], "Y")
     for name, g in zip(("dQ", "dK", "dV"), (rows(got[0]), *got[1:])):
         ref.close(g, want[name], name)
+
+
+@pytest.mark.parametrize("D", [16, 128])
+@pytest.mark.parametrize("scale,cap", [(1.0, 1e-6), (1e3, 1e-6), (1e4, 1e-2), (0.1, 1e-6), (30.0, 1e-4)])
+def test_caps_far_below_the_scale(scale, cap, D):
+    """Products bent from their last bits on: powers of scale / cap pass what fp32 holds."""
+    for Nq in (2, 150):
+        Q, K, V, dY, o = make(1, 2, 1, Nq, 200, D, seed=45, scale=scale, cap=cap)
+        K[:, :, ::3] = 0.0                        # scores of exactly zero
+        K[:, :, 1::3] *= 2.0 ** -20               # and some that the cap hardly bends
+        check(Q, K, V, dY, o)
+        K.mul_(0.0)                               # whole tiles of them
+        check(Q, K, V, dY, o)
