@@ -110,10 +110,10 @@ FLARE_API flare_status flare_qk_norm_rope_bwd(const flare_qk_norm_rope_args* arg
  * or an infinity in a row that takes part may also reach rows and keys that the
  * masks keep from it (0 times it is NaN, as in softmax(s) V).
  *
- * The cap is 0 or lies in [1e-6, 1e9]; Nq and Nk are at most 2^27.  Products
- * of bf16 rows, exponentials, sums and statistics are fp32; weights and dS
- * enter their products in bf16.  Gradients with respect to the slopes are not
- * computed.
+ * The scale is 0 or lies in [1e-30, 1e30], the cap is 0 or in [1e-6, 1e9]; Nq
+ * and Nk are at most 2^27.  Products of bf16 rows, exponentials, sums and
+ * statistics are fp32; weights and dS enter their products in bf16.  Gradients
+ * with respect to the slopes are not computed.
  *
  * Workspaces hold an error word in front (flare_last_device_status), the
  * documents' intervals, the partial results of splits along the keys, or the

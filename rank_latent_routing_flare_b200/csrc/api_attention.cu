@@ -123,6 +123,7 @@ flare_status fill_common(const flare_attention_args* a, bool backward, const voi
   if (!a->Q || !a->K || !a->V || !a->Y || !ws) return FLARE_ERR_NULL;
   if (a->prefix && !a->causal) return FLARE_ERR_SHAPE;
   if (!std::isfinite(a->scale) || !std::isfinite(a->cap)) return FLARE_ERR_SHAPE;
+  if (a->scale > 0.0 && (a->scale < 1e-30 || a->scale > 1e30)) return FLARE_ERR_UNSUPPORTED;   // what fp32 holds with room for products
   if (a->cap > 0.0 && (a->cap < 1e-6 || a->cap > 1e9)) return FLARE_ERR_UNSUPPORTED;   // what the tanh is accurate for
   st = tma_strides(r->q, a->Q, a->q_stride, a->B, a->Hq, a->Nq, a->D);
   if (st == FLARE_OK) st = tma_strides(r->k, a->K, a->k_stride, a->B, a->Hk, a->Nk, a->D);
