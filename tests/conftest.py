@@ -16,7 +16,14 @@ def pytest_configure(config):
 def pytest_collection_modifyitems(config, items):
     # A GPU test on a machine without CUDA is an error only if it was asked
     # for explicitly; under ``-m "not gpu"`` it is deselected anyway.
-    pass
+    #
+    # The other way round: this one makes valid calls with pointers that are
+    # not real, which find no device there; a device would read from them.
+    import torch
+    if torch.cuda.is_available():
+        for item in items:
+            if item.name.startswith("test_caps_and_lengths_out_of_range"):
+                item.add_marker(pytest.mark.skip(reason="a GPU is present: the pointers are not real"))
 
 
 @pytest.fixture(scope="session")
