@@ -58,6 +58,13 @@ def _refuse(name, t, dtype, shape, dev):
     raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def dense(t):
+    """A gradient as rows that the kernels can read: autograd may hand over fp32
+    tensors, expanded ones, and dense views at any offset of a larger one."""
+    t = t.to(_bf16).contiguous()
+    return t.clone() if t.data_ptr() & 15 else t
+
+
 def ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 

@@ -15,7 +15,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _binding as b
-from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, entry, output as _output, ptr, rows,
+from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, dense, entry, output as _output, ptr, rows,
                     workspace as _ws)
 
 # flare_attention_args
@@ -155,8 +155,7 @@ class Attention(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dY):
         Q, K, V, Y, L, *masks = ctx.saved_tensors
-        dY = dY.to(torch.bfloat16).contiguous()
-        dQ, dK, dV = flare_attention_bwd(Q, K, V, Y, L, dY, *masks, ctx.causal, ctx.scale, ctx.cap)
+        dQ, dK, dV = flare_attention_bwd(Q, K, V, Y, L, dense(dY), *masks, ctx.causal, ctx.scale, ctx.cap)
         return (dQ, dK, dV) + (None,) * 9
 
 

@@ -15,8 +15,8 @@ import struct
 import torch
 from torch.autograd.function import once_differentiable
 
-from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, entry, new_like, output as _output, ptr, rows,
-                    workspace as _ws)
+from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, dense, entry, new_like, output as _output, ptr,
+                    rows, workspace as _ws)
 
 # flare_qk_norm_rope_args
 _ARGS = struct.Struct("=9qd3q4q4q2q2q4q4q4q4q2q")
@@ -169,12 +169,11 @@ class QkNormRope(torch.autograd.Function):
 
 
 def _dense(dy, x):
-    """A gradient as rows the kernels can read (autograd may hand over expanded or fp32 tensors)."""
     if x is None:
         return None
     if dy is None:
         return torch.zeros(x.shape, dtype=torch.bfloat16, device=x.device)
-    return dy.to(torch.bfloat16).contiguous()
+    return dense(dy)
 
 
 def flare_qk_norm_rope(Q=None, K=None, q_gain=None, k_gain=None, freqs=None, positions=None, lengths=None,

@@ -167,3 +167,23 @@ def test_caps_far_below_the_scale(scale, cap, D):
         check(Q, K, V, dY, o)
         K.mul_(0.0)                               # whole tiles of them
         check(Q, K, V, dY, o)
+
+
+def test_gradients_that_arrive_off_a_16_byte_boundary():
+    """Autograd hands over dense views of larger gradients, at any offset."""
+    x = torch.randn(2, 2, 70, 32, device=DEV).bfloat16()
+    gain, odd = torch.ones(32, device=DEV), torch.zeros(3, dtype=torch.bfloat16, device=DEV)
+    w = torch.randn(3 + x.numel(), device=DEV).bfloat16()
+
+    def grads(f, cut):
+        leaf = x.clone().requires_grad_()
+        y = f(leaf).reshape(-1)
+        if cut:
+            torch.cat((odd, y)).backward(w)        # y's gradient is w[3:]
+        else:
+            y.backward(w[3:].clone())
+        return leaf.grad
+
+    for f in (lambda t: fl.flare_attention(t, t, t, causal=True), lambda t: fl.flare_qk_norm_rope(t, None, gain)[0],
+              lambda t: fl.flare_qk_norm_rope(None, t)[1]):
+        assert torch.equal(grads(f, True), grads(f, False))
