@@ -58,6 +58,14 @@ def _refuse(name, t, dtype, shape, dev):
     raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def no_gradient(what, **tensors):
+    """Refuses tensors that ask for a gradient which is not computed, where gradients are recorded."""
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{name}: gradients with respect to the {what} are not computed")
+
+
 def dense(t):
     """A gradient as rows that the kernels can read: autograd may hand over fp32
     tensors, expanded ones, and dense views at any offset of a larger one."""

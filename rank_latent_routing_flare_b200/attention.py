@@ -15,8 +15,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _binding as b
-from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, dense, entry, output as _output, ptr, rows,
-                    workspace as _ws)
+from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, dense, entry, no_gradient,
+                    output as _output, ptr, rows, workspace as _ws)
 
 # flare_attention_args
 _ARGS = struct.Struct("=7q2d12q6q4qq4q12q")
@@ -143,8 +143,6 @@ class Attention(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap):
-        if slopes is not None and slopes.requires_grad:
-            raise ValueError("slopes: gradients with respect to the distance bias are not computed")
         Y, L = flare_attention_fwd_train(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal,
                                          scale, cap)
         ctx.save_for_backward(Q, K, V, Y, L, lengths, q_lengths, q_offsets, documents, prefix, slopes)
@@ -162,4 +160,5 @@ class Attention(torch.autograd.Function):
 def flare_attention(Q, K, V, lengths=None, q_lengths=None, q_offsets=None, documents=None, prefix=None, slopes=None,
                     causal: bool = False, scale: float = 0.0, cap: float = 0.0):
     """Differentiable flare_attention_fwd (see Attention)."""
+    no_gradient("distance bias", slopes=slopes)
     return Attention.apply(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap)

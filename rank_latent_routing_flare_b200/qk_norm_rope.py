@@ -15,8 +15,8 @@ import struct
 import torch
 from torch.autograd.function import once_differentiable
 
-from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, dense, entry, new_like, output as _output, ptr,
-                    rows, workspace as _ws)
+from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, dense, entry, new_like, no_gradient,
+                    output as _output, ptr, rows, workspace as _ws)
 
 # flare_qk_norm_rope_args
 _ARGS = struct.Struct("=9qd3q4q4q2q2q4q4q4q4q2q")
@@ -152,9 +152,6 @@ class QkNormRope(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, Q, K, q_gain, k_gain, freqs, positions, lengths, eps, interleaved):
-        for name, t in (("freqs", freqs), ("positions", positions)):
-            if t is not None and t.requires_grad:
-                raise ValueError(f"{name}: gradients with respect to the angles are not computed")
         ctx.save_for_backward(Q, K, q_gain, k_gain, freqs, positions, lengths)
         ctx.eps, ctx.interleaved = eps, interleaved
         return flare_qk_norm_rope_fwd(Q, K, q_gain, k_gain, freqs, positions, lengths, eps, interleaved)
@@ -179,4 +176,5 @@ def _dense(dy, x):
 def flare_qk_norm_rope(Q=None, K=None, q_gain=None, k_gain=None, freqs=None, positions=None, lengths=None,
                        eps: float = 1e-6, interleaved: bool = False):
     """Differentiable flare_qk_norm_rope_fwd (see QkNormRope)."""
+    no_gradient("angles", freqs=freqs, positions=positions)
     return QkNormRope.apply(Q, K, q_gain, k_gain, freqs, positions, lengths, eps, interleaved)

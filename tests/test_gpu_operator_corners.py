@@ -187,3 +187,21 @@ def test_gradients_that_arrive_off_a_16_byte_boundary():
     for f in (lambda t: fl.flare_attention(t, t, t, causal=True), lambda t: fl.flare_qk_norm_rope(t, None, gain)[0],
               lambda t: fl.flare_qk_norm_rope(None, t)[1]):
         assert torch.equal(grads(f, True), grads(f, False))
+
+
+def test_learned_biases_and_angles_without_gradients():
+    """Slopes, frequencies and positions that ask for gradients are refused only where gradients are recorded."""
+    x = torch.randn(1, 2, 50, 32, device=DEV).bfloat16()
+    slopes = torch.tensor([0.1, 0.2], device=DEV, requires_grad=True)
+    freqs = torch.rand(2, 16, device=DEV, requires_grad=True)
+    coords = torch.rand(1, 50, 2, device=DEV, requires_grad=True)
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            assert torch.equal(fl.flare_attention(x, x, x, slopes=slopes), fl.flare_attention_fwd(x, x, x, slopes=slopes))
+            assert torch.equal(fl.flare_qk_norm_rope(x, None, None, None, freqs, coords)[0],
+                               fl.flare_qk_norm_rope_fwd(x, None, None, None, freqs, coords)[0])
+    with pytest.raises(ValueError):
+        fl.flare_attention(x, x, x, slopes=slopes)
+    for f, p in ((freqs, coords.detach()), (freqs.detach(), coords)):
+        with pytest.raises(ValueError):
+            fl.flare_qk_norm_rope(x, None, None, None, f, p)
