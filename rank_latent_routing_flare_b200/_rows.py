@@ -101,22 +101,30 @@ def call(name, where, dev, stream, *args):
         raise b.FlareError(st, where)
 
 
-# Memory that a call allocates for work on another stream than the current one
-# is recorded there, so that it is not handed out again before that work is done.
+# What a call allocates for work on another stream than the current one comes
+# from that stream's memory: a block that was freed on the current one may still
+# be read by work queued there.  Outputs are recorded on the current stream,
+# where the caller goes on with them.
+
+def new(make, stream):
+    """make(), a new output of a call on `stream` (None: the current one)."""
+    if stream is None:
+        return make()
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(here)
+    return t
+
 
 def new_like(like, stream):
-    t = empty_like(like, memory_format=_dense)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+    return new(lambda: empty_like(like, memory_format=_dense), stream)
 
 
 def output(name, t, like, dev, stream, check):
     """An output of `like`'s shape, new unless given, and its pointer and strides."""
     if t is None:
-        t = empty_like(like, memory_format=_dense)
-        if stream is not None:
-            t.record_stream(stream)
+        t = empty_like(like, memory_format=_dense) if stream is None else new_like(like, stream)
     elif check:
         return t, check_rows(name, t, like.shape, dev, output=True)
     return (t, (t.data_ptr(), *t.stride()[:3]))
@@ -125,10 +133,10 @@ def output(name, t, like, dev, stream, check):
 def workspace(ws, nbytes, like, stream):
     """The caller's workspace, checked, or a new one."""
     if ws is None:
-        ws = torch.empty(nbytes if nbytes > 256 else 256, dtype=torch.uint8, device=like.device)
         if stream is not None:
-            ws.record_stream(stream)
-        return ws
+            with torch.cuda.stream(stream):
+                return workspace(None, nbytes, like, None)
+        return torch.empty(nbytes if nbytes > 256 else 256, dtype=torch.uint8, device=like.device)
     check_small("workspace", ws, torch.uint8, None, like.get_device())
     if ws.numel() < nbytes:
         raise ValueError(f"workspace has {ws.numel()} bytes, needs {nbytes}")

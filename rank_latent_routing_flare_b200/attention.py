@@ -15,7 +15,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _binding as b
-from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, dense, entry, no_gradient,
+from ._rows import (NO_ROWS, ROW_WIDTHS, call, check_rows, check_small, dense, entry, new, no_gradient,
                     output as _output, ptr, rows, workspace as _ws)
 
 # flare_attention_args
@@ -104,9 +104,7 @@ def flare_attention_fwd_train(Q, K, V, lengths=None, q_lengths=None, q_offsets=N
                               L_out=None, workspace=None, stream=None, check: bool = True, device_check: bool = False):
     """flare_attention_fwd that returns (Y, L), what flare_attention_bwd takes."""
     if L_out is None:
-        L_out = torch.empty(Q.shape[:3], dtype=_f32, device=Q.device)
-        if stream is not None:
-            L_out.record_stream(stream)
+        L_out = new(lambda: torch.empty(Q.shape[:3], dtype=_f32, device=Q.device), stream)
     Y = flare_attention_fwd(Q, K, V, lengths, q_lengths, q_offsets, documents, prefix, slopes, causal, scale, cap, Y,
                             L_out, workspace, stream, check, device_check)
     return Y, L_out

@@ -205,3 +205,36 @@ def test_learned_biases_and_angles_without_gradients():
     for f, p in ((freqs, coords.detach()), (freqs.detach(), coords)):
         with pytest.raises(ValueError):
             fl.flare_qk_norm_rope(x, None, None, None, f, p)
+
+
+def test_memory_of_a_call_on_another_stream_is_not_taken_early():
+    """A call on another stream does not write into memory that work queued on the current one still reads."""
+    B, N, H, D = 1, 5000, 2, 64
+    x = torch.randn(B, H, N, D, device=DEV).bfloat16()
+    few, gain, freqs = x[:, :, :1], torch.ones(D, device=DEV), torch.rand(D // 2, device=DEV)
+    Y, L = fl.flare_attention_fwd_train(x, x, x)
+    side = torch.cuda.Stream()
+    calls = {
+        "rows": lambda: fl.flare_qk_norm_rope_fwd(x, x, gain, gain, freqs, stream=side),
+        "gradients": lambda: fl.flare_qk_norm_rope_bwd(x, x, x, x, gain, gain, freqs, stream=side),
+        "attention": lambda: fl.flare_attention_fwd_train(x, x, x, stream=side),
+        "few": lambda: fl.flare_attention_fwd(few, x, x, stream=side),
+        "backward": lambda: fl.flare_attention_bwd(x, x, x, Y, L, x, stream=side),
+    }
+    sizes = [x.numel() * 2, L.numel() * 4, gain.numel() * 4, few.numel() * 2, 256,
+             fl.flare_attention_workspace_bytes(B, H, H, N, N, D), fl.flare_attention_workspace_bytes(B, H, H, 1, N, D),
+             fl.flare_attention_workspace_bytes(B, H, H, N, N, D, True), fl.flare_qk_norm_rope_workspace_bytes(B, N, H, H, D)]
+    for name, call in calls.items():
+        call()
+        torch.cuda.synchronize()
+        held = [torch.full((n,), 77, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(4)]
+        copies = [torch.empty_like(t) for t in held]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(40_000_000)                                   # some 20 ms
+        for c, t in zip(copies, held):
+            c.copy_(t)
+        del held, c, t                                                  # freed, and still to be read
+        out = call()
+        torch.cuda.synchronize()
+        assert all((c == 77).all() for c in copies), name
+        del out
