@@ -47,7 +47,8 @@ extern "C" {
  *   pos_kind 0: pos[n] = n                          (axes 1, positions NULL)
  *   pos_kind 1: positions int32 [B][N]              (axes 1)
  *   pos_kind 2: positions float [B][N][axes]        (axes 1 .. 4)
- * gain: float [D], or [H][D] when gain_per_head; NULL: no gain.
+ * gain: float [D], or [H][D] when gain_per_head; NULL: no gain.  Gains and
+ * their gradients lie on 16-byte boundaries.
  * lengths: optional int32 [B], clamped to [0, N]; rows n >= lengths[b] are
  * not read and are written as zeros.
  */

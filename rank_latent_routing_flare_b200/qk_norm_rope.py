@@ -32,7 +32,13 @@ def flare_qk_norm_rope_workspace_bytes(B: int, N: int, Hq: int, Hk: int, D: int)
 def _check_gain(name, g, H, D, dev):
     if H == 0:
         raise ValueError(f"{name} is given without its tensor")
-    return check_small(name, g, _f32, (D,) if g.dim() == 1 else (H, D), dev)
+    return _aligned(name, check_small(name, g, _f32, (D,) if g.dim() == 1 else (H, D), dev))
+
+
+def _aligned(name, p):
+    if p & 15:
+        raise ValueError(f"{name} must lie on a 16-byte boundary")
+    return p
 
 
 def _head(Q, K, q_gain, k_gain, freqs, positions, lengths, eps, interleaved, check):
@@ -101,11 +107,11 @@ def flare_qk_norm_rope_fwd(Q=None, K=None, q_gain=None, k_gain=None, freqs=None,
     of y are rotated by the angles positions @ freqs.  Returns (Qr, Kr),
     head-major bf16 (or the given outputs).
 
-    gains: float32 [D] or [H, D].  freqs: float32 [rot/2] or [axes, rot/2];
-    None: no rotation.  positions: None (the token index), int32 [B, N], or
-    float32 [B, N, axes] coordinates.  Pairs are (p, p + rot/2), with rot a
-    multiple of 16, or (2p, 2p + 1) when ``interleaved``.  Rows n >=
-    lengths[b] (int32 [B]) are not read and come out as zeros."""
+    gains: float32 [D] or [H, D], on a 16-byte boundary.  freqs: float32
+    [rot/2] or [axes, rot/2]; None: no rotation.  positions: None (the token
+    index), int32 [B, N], or float32 [B, N, axes] coordinates.  Pairs are (p, p +
+    rot/2), with rot a multiple of 16, or (2p, 2p + 1) when ``interleaved``.
+    Rows n >= lengths[b] (int32 [B]) are not read and come out as zeros."""
     head, (*_, dev) = _head(Q, K, q_gain, k_gain, freqs, positions, lengths, eps, interleaved, check)
     Qr, q = _side("Qr", Qr, Q, dev, stream, check)
     Kr, k = _side("Kr", Kr, K, dev, stream, check)
@@ -136,7 +142,7 @@ def flare_qk_norm_rope_bwd(Q=None, K=None, dQr=None, dKr=None, q_gain=None, k_ga
         elif g.get(name) is None:
             g[name] = new_like(gain, stream)
         elif check:
-            check_small(name, g[name], _f32, gain.shape, dev)
+            _aligned(name, check_small(name, g[name], _f32, gain.shape, dev))
     ws, nbytes = 0, 0
     if q_gain is not None or k_gain is not None:
         workspace = _ws(workspace, flare_qk_norm_rope_workspace_bytes(B, N, Hq, Hk, D), Q if Q is not None else K,

@@ -238,3 +238,13 @@ def test_memory_of_a_call_on_another_stream_is_not_taken_early():
         torch.cuda.synchronize()
         assert all((c == 77).all() for c in copies), name
         del out
+
+
+def test_gains_off_a_16_byte_boundary_are_named():
+    x = torch.randn(1, 2, 40, 32, device=DEV).bfloat16()
+    off, ok = torch.ones(33, device=DEV)[1:], torch.ones(32, device=DEV)
+    for bad in (dict(Q=x, q_gain=off), dict(K=x, k_gain=off), dict(K=x, k_gain=torch.ones(65, device=DEV)[1:].view(2, 32))):
+        with pytest.raises(ValueError, match="_gain.*16-byte"):
+            fl.flare_qk_norm_rope_fwd(**bad)
+    with pytest.raises(ValueError, match="dq_gain.*16-byte"):
+        fl.flare_qk_norm_rope_bwd(x, None, x, None, ok, grads={"dq_gain": torch.empty(33, device=DEV)[1:]})
