@@ -21,7 +21,7 @@ __device__ __noinline__ float largest_score(const AttnBwdParams& bp, int b, int 
   for (int j = iv.x + l; j < iv.y; j += D / 8) {
     const uint4* kj = reinterpret_cast<const uint4*>(k + j * bp.k.sn);
     float s = 0.f;
-#pragma unroll
+#pragma unroll 2
     for (int c = 0; c < D / 8; ++c) {
       const uint4 x = q[c], y = kj[c];
       const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
@@ -37,8 +37,8 @@ __device__ __noinline__ float largest_score(const AttnBwdParams& bp, int b, int 
 // One row's statistics: l2 = L log2(e), moved by the distance that the bias
 // positions leave out, and delta = <dY, Y> in fp32.  D / 8 lanes a row, 16-byte
 // loads.
-template <int D>
-__global__ void __launch_bounds__(256) attn_rows_kernel(const AttnBwdParams bp) {
+template <int D, bool BIAS>
+__global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ AttnBwdParams bp) {
   constexpr int L = D / 8, ROWS = 256 / L, T = BwdCfg<D, true>::T;
   const AttnParams& p = bp.a;
   const int rows = bp.row_blocks * T, blocks = (rows + ROWS - 1) / ROWS;
@@ -58,9 +58,12 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const AttnBwdParams bp) 
     for (int k = 0; k < 4; ++k) delta = fmaf(bf16_lo(u[k]), bf16_lo(v[k]), fmaf(bf16_hi(u[k]), bf16_hi(v[k]), delta));
   }
   const int pos = bias_position(m, i, iv);
-  const bool far = sees && p.slopes && fabsf(p.slopes[h] * bias_shift(m, i, iv)) > kFarBias;
-  float top = far ? largest_score<D>(bp, b, h, i, iv, pos, l) : 0.f;
-  if (__any_sync(~0u, far)) {
+  bool far = false;
+  float top = 0.f;
+  if constexpr (BIAS) {
+    far = sees && fabsf(p.slopes[h] * bias_shift(m, i, iv)) > kFarBias;
+    if (far) top = largest_score<D>(bp, b, h, i, iv, pos, l);
+    __syncwarp();
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
   }
@@ -70,7 +73,7 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const AttnBwdParams bp) 
     float l2 = INFINITY;
     if (sees) {
       float L2 = p.L[bh * p.mask.Nq + i];
-      if (p.slopes) L2 += p.slopes[h] * bias_shift(m, i, iv);
+      if (BIAS) L2 += p.slopes[h] * bias_shift(m, i, iv);
       if (far) l2 = top;
       else if (L2 != -INFINITY) l2 = L2 * kLog2e;
     }
@@ -99,7 +102,9 @@ cudaError_t launch_attn_rows(const AttnBwdParams& p, cudaStream_t s) {
   auto go = [&](auto d) {
     constexpr int D = decltype(d)::value, ROWS = 256 / (D / 8);
     const long blocks = (static_cast<long>(p.row_blocks) * BwdCfg<D, true>::T + ROWS - 1) / ROWS;
-    attn_rows_kernel<D><<<static_cast<unsigned>(blocks * p.a.B * p.a.Hq), 256, 0, s>>>(p);
+    const unsigned grid = static_cast<unsigned>(blocks * p.a.B * p.a.Hq);
+    if (p.a.slopes) attn_rows_kernel<D, true><<<grid, 256, 0, s>>>(p);
+    else attn_rows_kernel<D, false><<<grid, 256, 0, s>>>(p);
     return cudaGetLastError();
   };
   switch (p.a.D) {
