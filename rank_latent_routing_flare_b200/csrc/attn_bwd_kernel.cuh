@@ -580,8 +580,15 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
       }
     }
   }
+  // TMEM is given back before the CTA waits for the others of its cluster: one
+  // that has not begun may be waiting for columns that depend on these
   tc_fence_before();
   __syncthreads();
+  if (warp == Cfg::MMAS) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::TMEM_COLS);
+  }
+  __syncwarp();
   if (KV && splits > 1) {   // each CTA of the cluster adds up its share of the rows, in the splits' order
     cluster_sync();
     const int per = 128 / splits;
@@ -609,10 +616,6 @@ __global__ void __launch_bounds__(BwdCfg<D, KV>::THREADS, BwdCfg<D, KV>::CTAS)
     for (int st = 0; st < NST; ++st)
       if (last_load[st] >= 0) mbar_wait_drain(y_full + st, (last_load[st] / NST) & 1, p.timeout_ns);
     if (!Cfg::XT) mbar_wait_drain(x_full, 0, p.timeout_ns);
-  }
-  if (warp == Cfg::MMAS) {
-    tc_fence_after();
-    tmem_dealloc(tmem, Cfg::TMEM_COLS);
   }
 }
 

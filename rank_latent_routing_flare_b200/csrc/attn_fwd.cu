@@ -569,6 +569,14 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
       }
     }
   }
+  // TMEM is given back before the CTA waits for the others of its cluster: one
+  // that has not begun may be waiting for columns that depend on these
+  tc_fence_before();
+  __syncthreads();
+  if (warp == Cfg::MMAS) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::TMEM_COLS);
+  }
   if (p.splits > 1 && p.splits <= kAttnClusterSplits) {
     __syncwarp();
     cluster_sync();
@@ -584,16 +592,10 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
     __syncwarp();
     cluster_sync();   // the others have read this CTA's rows
   }
-  tc_fence_before();
-  __syncthreads();
   if (warp == Cfg::LOADS && lane == 0 && ntiles > 0) {   // copies still in flight (only after an abort) must land before exit
     for (int st = 0; st < NST; ++st)
       if (last_load[st] >= 0) mbar_wait_drain(kv_full + st, (last_load[st] / NST) & 1, p.timeout_ns);
     for (int w = 0; w < NQ; ++w) mbar_wait_drain(q_full + w, 0, p.timeout_ns);
-  }
-  if (warp == Cfg::MMAS) {
-    tc_fence_after();
-    tmem_dealloc(tmem, Cfg::TMEM_COLS);
   }
 }
 

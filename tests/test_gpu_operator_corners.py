@@ -248,3 +248,33 @@ def test_gains_off_a_16_byte_boundary_are_named():
             fl.flare_qk_norm_rope_fwd(**bad)
     with pytest.raises(ValueError, match="dq_gain.*16-byte"):
         fl.flare_qk_norm_rope_bwd(x, None, x, None, ok, grads={"dq_gain": torch.empty(33, device=DEV)[1:]})
+
+
+def test_mixer_and_split_attention_at_once():
+    """The mixer's kernels and attention whose clusters join their splits, on two streams: neither waits for columns
+    of TMEM that the other holds until a third has run."""
+    g = torch.Generator(device=DEV).manual_seed(46)
+    K, V = (torch.randn(1, 8, 60000, 16, generator=g, device=DEV).bfloat16() for _ in range(2))
+    latents = torch.randn(8, 64, 16, generator=g, device=DEV).bfloat16()
+    jobs = [make(1, 4, 2, 512, 2000, 32, seed=47), make(1, 8, 1, 700, 700, 32, seed=48, causal=True),
+            make(1, 8, 1, 700, 700, 64, seed=49, causal=True), make(1, 2, 2, 600, 1500, 64, seed=50)]
+
+    def attend():
+        out = []
+        for Q, k, v, dY, o in jobs:
+            Y, L = fl.flare_attention_fwd_train(Q, k, v, **o)
+            out += [Y, L, *fl.flare_attention_bwd(Q, k, v, Y, L, dY, **o)]
+        return out
+
+    want, mixed = attend(), fl.flare_mixer_fwd(K, V, latents, device_check=False)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for s in streams[:2]:
+            with torch.cuda.stream(s):
+                got.append(attend())
+        with torch.cuda.stream(streams[2]):
+            ys = [fl.flare_mixer_fwd(K, V, latents, device_check=False) for _ in range(6)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for x in got for a, b in zip(x, want)) and all(torch.equal(y, mixed) for y in ys)
