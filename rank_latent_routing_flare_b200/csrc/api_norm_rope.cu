@@ -8,8 +8,8 @@
 namespace flare {
 namespace {
 
-// Sizes the kernels cover: the angles, the accumulators of the gains'
-// gradients (4 bytes a column, 128 KB of shared memory) and the grid.
+// Sizes the kernels cover.  32768 columns: every CTA leaves a partial row of
+// the gains' gradients, 40 MB of workspace for two CTAs an SM.
 flare_status check_sizes(int64_t B, int64_t N, int64_t Hq, int64_t Hk, int64_t D) {
   if (B < 1 || N < 1 || Hq < 0 || Hk < 0 || Hq + Hk < 1) return FLARE_ERR_SHAPE;
   if (!row_width_ok(D)) return FLARE_ERR_UNSUPPORTED;

@@ -1,5 +1,5 @@
 // Parameters of the exact softmax attention kernels (attn_fwd.cu,
-// attn_step.cu, attn_bwd.cu, attn_rows.cu).
+// attn_step.cu, attn_bwd_dq.cu, attn_bwd_dkv.cu).
 #pragma once
 
 #include <cstdint>

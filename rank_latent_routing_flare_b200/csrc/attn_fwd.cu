@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
   // last one down under a distance bias, whose rows then meet their nearest
   // keys early and raise their reference no more (a causal mask puts those
   // last).  Each query tile takes part in steps [a, e).
-  int a[2] = {range[0], NQ == 2 ? range[2] : 0}, e[2] = {range[1], NQ == 2 ? range[3] : 0};
+  int a[2] = {range[0], range[2]}, e[2] = {range[1], range[3]};
   int jlo, jhi;
   {
     const bool live0 = a[0] < e[0], live1 = a[1] < e[1];
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
           __syncwarp();
           return true;
         };
-        bool ok = mbar_wait_warp(q_full, 0, wc) && (NQ == 1 || mbar_wait_warp(q_full + 1, 0, wc));
+        bool ok = mbar_wait_warp(q_full, 0, wc) && mbar_wait_warp(q_full + 1, 0, wc);
         int used[2] = {0, 0};
 #pragma unroll
         for (int w = 0; w < NQ; ++w)
@@ -439,11 +439,13 @@ __global__ void __launch_bounds__(FwdCfg<D, MOD>::THREADS, FwdCfg<D, MOD>::CTAS)
       } else if (MOD == 1) {
         // tanh grows with its argument: the maximum takes it once.  D <= 64:
         // hidden columns count too (under a cap of up to 55 they lie at most
-        // 2^80 above the others, which no fp32 or bf16 weight minds) and get
-        // their zeros behind the exponential: 12 documents in 8192 keys 177 -> 162
-        // us.  A row's largest weight is then no exact 1: its rounding to bf16 adds
-        // up to as much again as the output's.  At D = 128 the second body costs
-        // more than it saves (prefixes 208 -> 215).
+        // 2^37 above 1, half the cap, and the row's own keys at least 2^-80, which
+        // leaves weights of 2^-117 to fp32 and bf16) and get their zeros behind
+        // the exponential: the same 12 documents in 8192 keys, a whole call, 205
+        // -> 190 us.  A row's largest weight is then no exact 1 and is rounded to
+        // bf16 like the others: relative error of Y 0.0018 -> 0.0021, of which
+        // its own rounding is 0.0016.  At D = 128 the second body costs more than
+        // it saves (prefixes 208 -> 215).
         mx = max_of(s);
         const bool poly = __all_sync(~0u, ops.small(fmaxf(mx, -min_of(s))));
         small = poly && (!masked || (D < 128 && ops.out <= 80.f));
