@@ -110,10 +110,9 @@ def new(make, stream):
     """make(), a new output of a call on `stream` (None: the current one)."""
     if stream is None:
         return make()
-    here = torch.cuda.current_stream(stream.device)
     with torch.cuda.stream(stream):
         t = make()
-    t.record_stream(here)
+    t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
 

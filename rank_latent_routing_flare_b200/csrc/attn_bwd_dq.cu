@@ -10,7 +10,7 @@ namespace {
 // its keys that L, about -slope times that distance, has no bits left for the
 // scores (the dQ pass divides by the sum of the weights in any case).  Slow,
 // and rare: a row 2^24 / slope tokens or more from the nearest key it sees.
-constexpr float kFarBias = 0x1p24f;   // up to here L is off by one at most
+constexpr float kFarBias = 0x1p24f;   // up to here L is off by a few units, weights by e^3
 template <int D>
 __device__ __noinline__ float largest_score(const AttnBwdParams& bp, int b, int h, int i, int2 iv, int pos, int l) {
   const AttnParams& p = bp.a;
