@@ -45,8 +45,8 @@
 // D >= 64: T = 64, up to 512 TMEM columns, one CTA per SM.  D <= 32: T = 48, 256
 // columns, two CTAs per SM; the exponentials bound those.  Measured, dQ and
 // dK/dV pass: D = 128, 2 x 16 heads (4 key heads) x 4095^2, capped, causal with
-// prefixes 317 and 316 us (0.94 PFLOP/s over their four products each); D = 32,
-// 8 x 8 heads x 4096^2, ragged, 221 and 296.
+// prefixes 324 and 312 us (0.94 PFLOP/s over their four products each); D = 32,
+// 8 x 8 heads x 4096^2, ragged, 222 and 294.
 #pragma once
 
 #include <tuple>

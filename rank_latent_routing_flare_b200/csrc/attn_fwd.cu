@@ -31,8 +31,8 @@
 // D = 128, and capped or biased scores: KT = 128, 512 TMEM columns, one CTA per
 // SM whose softmax threads take over most of its registers.  Plain scores of D
 // <= 64: KT = 64 and 256 columns let two CTAs share an SM.  Measured on 2 x 16
-// heads x 4096^2, D = 64: plain 231 us (one CTA: 254), capped 303 (two CTAs,
-// which spill: 364), biased 303 (337); D = 128: plain 291, capped 325.
+// heads x 4096^2, D = 64: plain 228 us (one CTA: 254), capped 300 (two CTAs,
+// which spill: 364), biased 286 (337); D = 128: plain 289, capped 332.
 #include <utility>
 
 #include "attn_common.cuh"
